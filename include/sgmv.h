@@ -3,7 +3,9 @@
  *
  * Operation (wiki page "Implementation: Predibase Lorax SGMV Expand Slice
  * Kernel", Description and I/O Contract), and the LoRA-A projection that
- * produces its inputs (sgmv_shrink, below): for each segment b of a packed
+ * produces its inputs (sgmv_shrink, below); further down the operators a
+ * serving step runs beside them (sgmv_lora_linear, sgmv_grouped_gemm,
+ * sgmv_route, sgmv_combine).  The expand: for each segment b of a packed
  * batch and each token m of that segment, row t = b_seq_start_loc[b] + m of
  * the output gets, in its column window [slice_offset, slice_offset +
  * slice_size),
@@ -34,13 +36,16 @@
 extern "C" {
 #endif
 
-#define SGMV_ABI_VERSION 5
+#define SGMV_ABI_VERSION 6
 #define SGMV_MAX_SLICES 8      /* slices per multi-slice call                       */
 #define SGMV_MAX_RANK 256      /* largest rank the register-tiled kernels take; larger
                                   ranks (any size) run on the generic kernel */
 #define SGMV_MAX_FUSED_SLICES 3 /* slices per fused shrink-expand call (QKV, gate/up) */
 #define SGMV_MAX_BATCHES 4000  /* segment table lives in on-chip memory (LDS, 64 KiB);
                                   also the most tokens of one per-token call */
+
+#define SGMV_MAX_EXPERTS 1024  /* experts of a routing call                         */
+#define SGMV_MAX_TOP_K 32      /* choices of a token in a routing call              */
 
 /* Element types (I/O Contract: weights float16/bfloat16; inputs
  * float16/bfloat16/float32). */
@@ -339,6 +344,158 @@ sgmv_status sgmv_fused_shrink_expand(sgmv_matrix inputs, const sgmv_fused_slice*
                                      const int64_t* lora_indices, int64_t batches,
                                      int64_t max_seq_len, float scale, int add_inputs,
                                      hipStream_t stream);
+
+/*
+ * sgmv_lora_linear -- a shared projection with the low-rank adapters of many
+ * requests beside it: what a serving step runs at each adapted layer, where
+ * sgmv_shrink and sgmv_expand_* compute the adapters' part alone.  For every
+ * row t of out,
+ *
+ *     out[t][n] = (add_inputs ? out[t][n] : 0) + bias[n]
+ *                 + sum_h inputs[t][h] * weight[n][h]
+ *                 + sum_k v_s[t][k] * lora_b_s[a][n - off_s][k],
+ *     v_s[t][k] = scale * sum_h inputs[t][h] * lora_a_s[a][k][h],
+ *
+ * the last sum where slice s's window [off_s, off_s + slice_size) holds n and
+ * t lies in a segment b with a = lora_indices[b] != -1.  Every row gets the
+ * shared projection: also rows of index -1 segments (requests without an
+ * adapter), rows outside every segment, and all rows when num_slices or
+ * batches is 0.  Sums in fp32, one rounding (nearest even) to the output
+ * dtype; v_s is kept in fp32 and enters the second product as two 16-bit
+ * parts, so it is not rounded to the weights' dtype (with float16 weights
+ * a |v_s| above 65504 becomes an infinity).
+ *
+ * inputs        device (total_tokens, hidden) f16/bf16; read only.
+ * weight        device (out.cols, hidden), the inputs' dtype, row_stride >=
+ *               hidden; read only.
+ * bias          device (out.cols) of the weight's dtype, or NULL.
+ * slices        host array of 0..SGMV_MAX_SLICES descriptors, read during
+ *               the call only: lora_a (lora_num, rank, hidden) and lora_b
+ *               (lora_num, slice_size, rank), contiguous, device, of the
+ *               weight's dtype, one rank (<= SGMV_MAX_RANK) and one lora_num;
+ *               windows must not overlap.
+ * out           device (total_tokens, out_cols) f16/bf16/f32, row_stride >=
+ *               cols; must not overlap any other argument.
+ * b_seq_start_loc, seq_lens, lora_indices, batches, max_seq_len, stream:
+ *               as for sgmv_expand_slice, with the same device-side
+ *               preconditions (a segment that breaks one gets the shared
+ *               projection alone).
+ * scale         fp32 factor of the adapters' part.
+ * add_inputs    nonzero: accumulate onto out; zero: overwrite.
+ * workspace, workspace_bytes:
+ *               device buffer of at least sgmv_lora_linear_workspace_bytes()
+ *               bytes, 16-byte aligned, any contents (the projected rows
+ *               v_s); may be NULL when no slice or no segment is given.
+ *               Calls that may run at the same time need buffers of their
+ *               own; it must not overlap any other argument.
+ *
+ * Returns SGMV_OK, or a status with nothing launched; total_tokens == 0 or
+ * out.cols == 0 return SGMV_OK without a launch.
+ */
+sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void* bias,
+                             const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
+                             const int64_t* b_seq_start_loc, const int64_t* seq_lens,
+                             const int64_t* lora_indices, int64_t batches, int64_t max_seq_len,
+                             float scale, int add_inputs, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of the workspace sgmv_lora_linear takes. */
+sgmv_status sgmv_lora_linear_workspace_bytes(int64_t tokens, int num_slices, int64_t rank,
+                                             size_t* bytes);
+
+/*
+ * sgmv_grouped_gemm -- matrix products grouped by expert with ragged sizes:
+ * the segmented product with whole weight matrices in the adapters' place.
+ * For every row r of a segment b with e = expert_indices[b] (b itself when
+ * expert_indices is NULL),
+ *
+ *     y[n] = sum_h inputs[src(r)][h] * weights[e][n][h],
+ *     out[r][n] = y[n]                                  (gated == 0), or
+ *     out[r][n] = y[n] / (1 + exp(-y[n])) * y[out.cols + n]   (gated != 0),
+ *
+ * with src(r) = row_indices[r], or r when row_indices is NULL.  gated: a
+ * weight matrix holds the gate's rows, then as many rows of the other factor
+ * (the gate/up products of an expert with its SiLU gate, in one launch).
+ * Sums in fp32, one rounding (nearest even) to the output dtype.  Rows of
+ * index -1 segments and rows outside every segment are left untouched.
+ *
+ * inputs        device (input_rows, hidden) f16/bf16; read only.
+ * weights       device (experts, out.cols or 2 * out.cols, hidden) of the
+ *               inputs' dtype, contiguous; read only.
+ * out           device (rows, out_cols) f16/bf16/f32, row_stride >= cols; must
+ *               not overlap any other argument.
+ * row_indices   device int64[rows] or NULL (then input_rows == rows); read
+ *               only at rows of active segments.  A row whose index lies
+ *               outside [0, input_rows) is the product of a row of zeros.
+ * expert_indices  device int64[batches] or NULL.
+ * b_seq_start_loc, seq_lens, batches, max_seq_len, stream: as for
+ *               sgmv_expand_slice, with the same device-side preconditions.
+ *               sgmv_route writes them for a batch of routed tokens.
+ *
+ * Returns SGMV_OK, or a status with nothing launched; batches == 0, no
+ * expert, no row or no column return SGMV_OK without a launch.
+ */
+sgmv_status sgmv_grouped_gemm(sgmv_matrix inputs, sgmv_stack weights, sgmv_matrix out,
+                              const int64_t* row_indices, const int64_t* b_seq_start_loc,
+                              const int64_t* seq_lens, const int64_t* expert_indices,
+                              int64_t batches, int64_t max_seq_len, int gated,
+                              hipStream_t stream);
+
+/*
+ * sgmv_route -- choose the experts of every token and lay the choices out as
+ * the segments that sgmv_grouped_gemm takes, without a copy to the host.
+ * Token t's choices j = 0..top_k-1 are its largest logits in descending
+ * order, ties to the lowest expert.  weights[t][j] is the softmax of the
+ * logits over all experts at that choice, or over the token's choices alone
+ * when renormalize is nonzero.  A logit of -inf or NaN closes the expert to
+ * the token: it is never chosen and adds nothing to the softmax.  A token
+ * with fewer open experts than top_k has experts -1, weights 0 and slots -1
+ * at the choices it lacks.  Where the largest logit is +inf, the experts at
+ * +inf share the weight.
+ *
+ * The choices are then ordered by (expert, token): slots[t][j] is the
+ * position of a choice, row_indices[slot] its token (-1 past the last
+ * choice), b_seq_start_loc[e] and seq_lens[e] expert e's run of slots.
+ *
+ * logits        device (tokens, experts) f16/bf16/f32, experts <=
+ *               SGMV_MAX_EXPERTS, row_stride >= experts; read only.
+ * top_k         1..min(experts, SGMV_MAX_TOP_K).
+ * weights       device float[tokens * top_k].
+ * experts, slots  device int64[tokens * top_k].
+ * row_indices   device int64[tokens * top_k].
+ * b_seq_start_loc, seq_lens  device int64[experts].
+ * workspace     device buffer of sgmv_route_workspace_bytes() bytes, 16-byte
+ *               aligned, any contents; NULL when that is 0.
+ *
+ * The results do not depend on the order in which the GPU runs the work.
+ * Returns SGMV_OK, or a status with nothing launched; SGMV_ERR_UNSUPPORTED
+ * for more than 2^30 choices.
+ */
+sgmv_status sgmv_route(sgmv_matrix logits, int64_t top_k, int renormalize, float* weights,
+                       int64_t* experts, int64_t* slots, int64_t* row_indices,
+                       int64_t* b_seq_start_loc, int64_t* seq_lens, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of the workspace sgmv_route takes (0 for small batches). */
+sgmv_status sgmv_route_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k,
+                                       size_t* bytes);
+
+/*
+ * sgmv_combine -- the weighted sum of each token's expert rows,
+ *
+ *     out[t][n] = (add_inputs ? out[t][n] : 0)
+ *                 + sum_j weights[t][j] * rows[slots[t][j]][n]
+ *
+ * over the choices whose slot lies in [0, rows.rows) (others, such as -1,
+ * add nothing).  Sums in fp32 in order of j, one rounding (nearest even).
+ *
+ * rows          device (slots, hidden) f16/bf16/f32; read only.
+ * weights, slots  device float and int64 [tokens * top_k]; read only.
+ * out           device (tokens, hidden) f16/bf16/f32; must not overlap any
+ *               other argument.
+ */
+sgmv_status sgmv_combine(sgmv_matrix rows, const float* weights, const int64_t* slots,
+                         int64_t top_k, sgmv_matrix out, int add_inputs, hipStream_t stream);
 
 /* Message for the last non-OK status returned on the calling thread ("" if
  * none).  The pointer stays valid until the thread's next libsgmv call. */

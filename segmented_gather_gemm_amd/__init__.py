@@ -14,7 +14,10 @@ Lorax SGMV Expand Slice Kernel" (Signature; I/O Contract):
 
 plus the LoRA-A projection that produces those inputs (sgmv_shrink), the
 per-token and multi-slice forms, and the two steps fused in one launch
-(sgmv_fused_shrink_expand).
+(sgmv_fused_shrink_expand); and the operators a serving step runs beside them:
+a shared projection with the adapters (sgmv_lora_linear), products grouped by
+expert (sgmv_grouped_gemm), the routing that lays out their segments
+(sgmv_route) and the sum of a token's expert rows (sgmv_combine).
 """
 from __future__ import annotations
 
@@ -33,7 +36,10 @@ MAX_FUSED_SLICES = 3
 EXPORTED_SYMBOLS = ("sgmv_expand_slice", "sgmv_expand_multi_slice", "sgmv_bgmv_expand_slice",
                     "sgmv_shrink", "sgmv_shrink_multi_slice", "sgmv_shrink_workspace_bytes",
                     "sgmv_shrink_multi_slice_noalloc",
-                    "sgmv_fused_shrink_expand", "sgmv_last_error", "sgmv_abi_version")
+                    "sgmv_fused_shrink_expand", "sgmv_lora_linear",
+                    "sgmv_lora_linear_workspace_bytes", "sgmv_grouped_gemm", "sgmv_route",
+                    "sgmv_route_workspace_bytes", "sgmv_combine", "sgmv_last_error",
+                    "sgmv_abi_version")
 
 
 class Matrix(ctypes.Structure):
@@ -113,6 +119,22 @@ def _load_library() -> ctypes.CDLL:
                                              Matrix, p, p, p, i64, i64, ctypes.c_float,
                                              ctypes.c_int, p]
     lib.sgmv_fused_shrink_expand.restype = ctypes.c_int
+    lib.sgmv_lora_linear.argtypes = [Matrix, Matrix, p, ctypes.POINTER(FusedSliceDesc),
+                                     ctypes.c_int, Matrix, p, p, p, i64, i64, ctypes.c_float,
+                                     ctypes.c_int, p, ctypes.c_size_t, p]
+    lib.sgmv_lora_linear.restype = ctypes.c_int
+    lib.sgmv_lora_linear_workspace_bytes.argtypes = [i64, ctypes.c_int, i64,
+                                                     ctypes.POINTER(ctypes.c_size_t)]
+    lib.sgmv_lora_linear_workspace_bytes.restype = ctypes.c_int
+    lib.sgmv_grouped_gemm.argtypes = [Matrix, Stack, Matrix, p, p, p, p, i64, i64, ctypes.c_int,
+                                      p]
+    lib.sgmv_grouped_gemm.restype = ctypes.c_int
+    lib.sgmv_route.argtypes = [Matrix, i64, ctypes.c_int, p, p, p, p, p, p, p, ctypes.c_size_t, p]
+    lib.sgmv_route.restype = ctypes.c_int
+    lib.sgmv_route_workspace_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+    lib.sgmv_route_workspace_bytes.restype = ctypes.c_int
+    lib.sgmv_combine.argtypes = [Matrix, p, p, i64, Matrix, ctypes.c_int, p]
+    lib.sgmv_combine.restype = ctypes.c_int
     lib.sgmv_last_error.argtypes = []
     lib.sgmv_last_error.restype = ctypes.c_char_p
     lib.sgmv_abi_version.argtypes = []
@@ -439,12 +461,200 @@ def sgmv_fused_shrink_expand(inputs, slices: Sequence[Tuple[object, object, int]
     return output_tensor
 
 
+def _bytes_of(fn, *args) -> int:
+    n = ctypes.c_size_t()
+    rc = fn(*args, ctypes.byref(n))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return n.value
+
+
+def lora_linear_workspace_bytes(tokens: int, num_slices: int, rank: int) -> int:
+    """Bytes of the workspace sgmv_lora_linear takes."""
+    return _bytes_of(lib.sgmv_lora_linear_workspace_bytes, int(tokens), int(num_slices), int(rank))
+
+
+def route_workspace_bytes(tokens: int, experts: int, top_k: int) -> int:
+    """Bytes of the workspace sgmv_route takes (0 for small batches)."""
+    return _bytes_of(lib.sgmv_route_workspace_bytes, int(tokens), int(experts), int(top_k))
+
+
+def _scratch(device, workspace, need: int):
+    """(tensor to keep alive, pointer, bytes) of a call's scratch memory: the
+    caller's uint8 tensor, or None = taken from torch's allocator for this
+    call (it is stream-ordered, so the next user of the memory on this stream
+    comes after the call's kernels)."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = _torch.empty(need, dtype=_torch.uint8, device=device)
+    elif not _torch.is_tensor(workspace) or workspace.device != device or \
+            workspace.dtype != _torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def sgmv_lora_linear(inputs, weight, slices: Sequence[Tuple[object, object, int]], output_tensor,
+                     b_seq_start_loc, seq_len_tensor, lora_indices_tensor, batches: int,
+                     max_seq_length: int, scaling: float = 1.0, bias=None,
+                     add_inputs: bool = False, workspace=None):
+    """A shared projection with the adapters of many requests beside it:
+    output_tensor (+)= inputs @ weight.T + bias for every row, plus, for each
+    (lora_a_weights (lora_num, rank, hidden), lora_b_weights (lora_num,
+    slice_size, rank), slice_offset) in ``slices`` and every segment b with
+    index != -1, scaling * (inputs[rows] @ lora_a[idx].T) @ lora_b[idx].T in
+    the columns [slice_offset, slice_offset + slice_size).  One rounding;
+    ``slices`` may be empty.  Enqueued on the current stream.  `workspace`:
+    a uint8 tensor of lora_linear_workspace_bytes(), or None (taken from
+    torch's allocator for the call)."""
+    if len(slices) > MAX_SLICES:
+        raise ValueError(f"at most {MAX_SLICES} slices, got {len(slices)}")
+    device, (start, lens, idx) = _common(output_tensor, [
+        (b_seq_start_loc, "b_seq_start_loc"), (seq_len_tensor, "seq_len_tensor"),
+        (lora_indices_tensor, "lora_indices_tensor")])
+    if inputs.device != device or weight.device != device:
+        raise ValueError(f"inputs and weight must be on {device}")
+    if start.shape[0] < batches or lens.shape[0] < batches or idx.shape[0] < batches:
+        raise ValueError("segment metadata shorter than batches")
+    x = _matrix(inputs, "inputs")
+    w = _matrix(weight, "weight")
+    out = _matrix(output_tensor, "output_tensor")
+    bias_ptr = None
+    if bias is not None:
+        if bias.device != device or bias.dim() != 1 or bias.shape[0] != w.rows or \
+                bias.dtype != weight.dtype or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous ({w.rows},) {weight.dtype} tensor on "
+                             f"{device}")
+        bias_ptr = bias.data_ptr()
+    arr = (FusedSliceDesc * max(1, len(slices)))()
+    for i, (a, b, off) in enumerate(slices):
+        if a.device != device or b.device != device:
+            raise ValueError(f"slice {i} must be on {device}")
+        arr[i] = FusedSliceDesc(_stack_a(a, f"slice {i} lora_a"), _stack(b, f"slice {i} lora_b"),
+                                int(off))
+    need = 0
+    if slices and batches > 0 and workspace is None:
+        need = lora_linear_workspace_bytes(x.rows, len(slices), arr[0].lora_a.rows)
+    keep, ws, ws_bytes = _scratch(device, workspace, need)
+    rc = _call_on(device, lib.sgmv_lora_linear, x, w, bias_ptr, arr, len(slices), out,
+                  start.data_ptr(), lens.data_ptr(), idx.data_ptr(), int(batches),
+                  int(max_seq_length), float(scaling), int(bool(add_inputs)), ws, ws_bytes,
+                  _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return output_tensor
+
+
+def sgmv_grouped_gemm(inputs, expert_weights, output_tensor, b_seq_start_loc, seq_len_tensor,
+                      expert_indices_tensor, batches: int, max_seq_length: int,
+                      row_indices_tensor=None, gated: bool = False):
+    """Products grouped by expert, in place: for every row r of segment b with
+    expert e = expert_indices[b] (None: b itself), output_tensor[r] =
+    inputs[row_indices[r]] (None: inputs[r]) @ expert_weights[e].T;
+    expert_weights is (experts, columns, hidden).  ``gated``: the weights hold
+    2 * columns rows, gate first, and output_tensor[r] = silu(gate) * other.
+    Rows outside the segments and of index -1 ones are untouched.  Enqueued on
+    the current stream."""
+    metas = [(b_seq_start_loc, "b_seq_start_loc"), (seq_len_tensor, "seq_len_tensor")]
+    if expert_indices_tensor is not None:
+        metas.append((expert_indices_tensor, "expert_indices_tensor"))
+    device, kept = _common(output_tensor, metas)
+    if any(m.shape[0] < batches for m in kept):
+        raise ValueError("segment metadata shorter than batches")
+    if inputs.device != device or expert_weights.device != device:
+        raise ValueError(f"inputs and expert_weights must be on {device}")
+    x = _matrix(inputs, "inputs")
+    if expert_weights.dim() != 3 or not expert_weights.is_contiguous():
+        raise ValueError("expert_weights must be contiguous (experts, columns, hidden), got "
+                         f"{tuple(expert_weights.shape)}")
+    w = Stack(expert_weights.data_ptr(), _dtype_code(expert_weights), *expert_weights.shape)
+    out = _matrix(output_tensor, "output_tensor")
+    rows = None
+    if row_indices_tensor is not None:
+        rows = _meta(row_indices_tensor, "row_indices_tensor", device)
+        if rows.shape[0] < out.rows:
+            raise ValueError("row_indices_tensor shorter than the number of output rows")
+    rc = _call_on(device, lib.sgmv_grouped_gemm, x, w, out,
+                  None if rows is None else rows.data_ptr(), kept[0].data_ptr(),
+                  kept[1].data_ptr(), kept[2].data_ptr() if len(kept) > 2 else None, int(batches),
+                  int(max_seq_length), int(bool(gated)), _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return output_tensor
+
+
+def _flat(t, what: str, device, dtype, shape):
+    if t.device != device or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {shape} {dtype} tensor on {device}, got "
+                         f"{tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def sgmv_route(logits, weights, experts, slots, row_indices_tensor, b_seq_start_loc,
+               seq_len_tensor, renormalize: bool = False, workspace=None):
+    """Choose each token's experts and lay the choices out as the segments
+    sgmv_grouped_gemm takes, all on the device.  logits is (tokens, experts);
+    weights (float32), experts and slots (int64) are (tokens, top_k), written;
+    row_indices_tensor (tokens * top_k,), b_seq_start_loc and seq_len_tensor
+    (experts,) are int64, written.  Largest logits first, ties to the lowest
+    expert; softmax over all experts, or over the choices (``renormalize``);
+    -inf and NaN logits are closed, missing choices are -1 with weight 0.
+    Enqueued on the current stream.  `workspace`: a uint8 tensor of
+    route_workspace_bytes(), or None (taken from torch's allocator)."""
+    device = logits.device
+    if device.type != "cuda":
+        raise ValueError("logits must be a GPU tensor")
+    x = _matrix(logits, "logits")
+    if weights.dim() != 2 or weights.shape[0] != x.rows:
+        raise ValueError(f"weights must be ({x.rows}, top_k), got {tuple(weights.shape)}")
+    T, k, E = x.rows, weights.shape[1], x.cols
+    i64 = _torch.int64
+    ptrs = (_flat(weights, "weights", device, _torch.float32, (T, k)),
+            _flat(experts, "experts", device, i64, (T, k)),
+            _flat(slots, "slots", device, i64, (T, k)),
+            _flat(row_indices_tensor, "row_indices_tensor", device, i64, (T * k,)),
+            _flat(b_seq_start_loc, "b_seq_start_loc", device, i64, (E,)),
+            _flat(seq_len_tensor, "seq_len_tensor", device, i64, (E,)))
+    need = route_workspace_bytes(T, E, k) if workspace is None else 0
+    keep, ws, ws_bytes = _scratch(device, workspace, need)
+    rc = _call_on(device, lib.sgmv_route, x, k, int(bool(renormalize)), *ptrs, ws, ws_bytes,
+                  _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return weights, experts
+
+
+def sgmv_combine(expert_rows, weights, slots, output_tensor, add_inputs: bool = False):
+    """output_tensor[t] (+)= sum over j of weights[t, j] * expert_rows[slots[t, j]]
+    (slots outside expert_rows, such as -1, add nothing); weights float32 and
+    slots int64, both (tokens, top_k).  Enqueued on the current stream."""
+    device = output_tensor.device
+    if device.type != "cuda":
+        raise ValueError("output_tensor must be a GPU tensor")
+    if expert_rows.device != device:
+        raise ValueError(f"expert_rows must be on {device}")
+    rows = _matrix(expert_rows, "expert_rows")
+    out = _matrix(output_tensor, "output_tensor")
+    if weights.dim() != 2 or weights.shape[0] != out.rows:
+        raise ValueError(f"weights must be ({out.rows}, top_k), got {tuple(weights.shape)}")
+    k = weights.shape[1]
+    wp = _flat(weights, "weights", device, _torch.float32, (out.rows, k))
+    sp = _flat(slots, "slots", device, _torch.int64, (out.rows, k))
+    rc = _call_on(device, lib.sgmv_combine, rows, wp, sp, k, out, int(bool(add_inputs)),
+                  _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return output_tensor
+
+
 def abi_version() -> int:
     return lib.sgmv_abi_version()
 
 
 __all__ = ["sgmv_expand_slice", "sgmv_expand_multi_slice", "bgmv_expand_slice", "sgmv_shrink",
            "shrink_workspace_bytes", "sgmv_shrink_multi_slice_noalloc",
-           "sgmv_shrink_multi_slice", "sgmv_fused_shrink_expand", "abi_version", "SgmvError",
+           "sgmv_shrink_multi_slice", "sgmv_fused_shrink_expand", "sgmv_lora_linear", "lora_linear_workspace_bytes",
+           "sgmv_grouped_gemm", "sgmv_route", "route_workspace_bytes", "sgmv_combine",
+           "abi_version", "SgmvError",
            "lib", "Matrix", "Stack", "SliceDesc", "ShrinkSliceDesc", "FusedSliceDesc",
            "EXPORTED_SYMBOLS", "LIBRARY_PATH"]

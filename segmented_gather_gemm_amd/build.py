@@ -1,11 +1,11 @@
 """Build libsgmv.so in-tree with hipcc for gfx950 (MI355X).
 
-The library holds the C entry points (csrc/sgmv_api.cpp,
-csrc/sgmv_shrink_api.cpp, with shared helpers in csrc/sgmv_host.cpp) and the
-gfx950
+The library holds the C entry points (csrc/sgmv_*api.cpp, with shared
+helpers in csrc/sgmv_host.cpp) and the gfx950
 kernels (csrc/sgmv_fast_ks*.hip, csrc/sgmv_generic.hip, built from
 csrc/sgmv_device.h; csrc/sgmv_shrink_*.hip, built from csrc/sgmv_shrink.h;
-both on csrc/sgmv_common.h)
+csrc/sgmv_matmul_*.hip, built from csrc/sgmv_matmul.h; csrc/sgmv_route.hip;
+all on csrc/sgmv_common.h)
 with the code object embedded; nothing is
 compiled at run time.  Packed-fp32 VALU instructions are disabled for every
 HIP translation unit.
@@ -31,7 +31,8 @@ SOURCES = [os.path.join(CSRC, f) for f in
             "sgmv_shrink_generic.hip", "sgmv_shrink_k1.hip", "sgmv_shrink_k2.hip",
             "sgmv_shrink_k4.hip", "sgmv_shrink_k8.hip", "sgmv_shrink_k16.hip",
             "sgmv_fused_api.cpp", "sgmv_fused_k1.hip", "sgmv_fused_k2.hip", "sgmv_fused_k4.hip",
-            "sgmv_fused_k8.hip", "sgmv_valu.hip")]
+            "sgmv_fused_k8.hip", "sgmv_valu.hip", "sgmv_matmul_api.cpp",
+            "sgmv_matmul_generic.hip", "sgmv_route_api.cpp", "sgmv_route.hip")]
 
 STREAM_SOURCE = os.path.join(CSRC, "sgmv_stream.hip")
 STREAM_LIBRARY = os.path.join(HERE, "libsgmv_stream.so")

@@ -1,0 +1,208 @@
+// sgmv_matmul.h -- gfx950 device helpers of the shared projection with
+// adapters and of the grouped products: which tile a workgroup runs, which
+// adapter each of its rows has, and the result's last steps.  Internal to
+// libsgmv.
+#pragma once
+
+#include "sgmv_common.h"
+#include "sgmv_matmul_launch.h"
+
+namespace sgmv {
+namespace dev {
+
+// ---------------------------------------------------------------------------
+// Tiles.
+// ---------------------------------------------------------------------------
+
+// A workgroup's rows [row, end) of out with weight matrix `e`, and its
+// column tile; row < 0: nothing to do.
+struct TileLoc {
+  int32_t row, end, e, col;
+};
+
+// Position of workgroup `id` in the (row tile, column tile) grid.  Workgroups
+// go round-robin to the 8 XCDs, so XCD x = id mod 8 takes a contiguous eighth
+// of the order; in that order kGroupRows row tiles sweep the column tiles
+// together, so that the tiles an XCD runs at one time share a few weight and
+// input rows in its L2.
+constexpr uint32_t kGroupRows = 8;
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t row_tiles, uint32_t col_tiles,
+                                        int32_t* rt, int32_t* ct) {
+  const uint32_t U = row_tiles * col_tiles;
+  const uint32_t x = id & 7, j = id >> 3, share = U >> 3, extra = U & 7;
+  const uint32_t u = x * share + (x < extra ? x : extra) + j;
+  if (j >= share + (x < extra ? 1u : 0u)) {
+    *rt = -1;
+    *ct = 0;
+    return;
+  }
+  const uint32_t per_group = kGroupRows * col_tiles;
+  const uint32_t g = u / per_group, in = u - g * per_group;
+  const uint32_t left = row_tiles - g * kGroupRows;
+  const uint32_t rows = left < kGroupRows ? left : kGroupRows;
+  *ct = (int32_t)(in / rows);
+  *rt = (int32_t)(g * kGroupRows + in % rows);
+}
+
+// Row range and weight matrix of grouped segment b; tiles of `tile_rows`
+// rows it takes (0: inactive -- index out of range, empty, or outside
+// [0, T)).
+__device__ __forceinline__ int32_t read_group(const MatmulParams& p, int32_t b, int32_t tile_rows,
+                                              int32_t* row, int32_t* end, int32_t* e) {
+  const int64_t st = p.start[b], ln = p.lens[b];
+  const int64_t a = p.idx ? p.idx[b] : b;
+  const bool active = a >= 0 && a < p.L && ln > 0 && st >= 0 && st <= p.T - ln;
+  *row = active ? (int32_t)st : 0;
+  *end = active ? (int32_t)(st + ln) : 0;
+  *e = active ? (int32_t)a : 0;
+  return active ? (int32_t)((ln + tile_rows - 1) / tile_rows) : 0;
+}
+
+// The tile of this workgroup (all NT threads take part; `sh` holds
+// NT / 64 + 4 words of LDS).  Grouped: every workgroup counts the segments'
+// tiles (a block scan over contiguous runs of segments, so the order of
+// tiles is the order of segments), and the thread whose run holds the tile
+// looks it up.
+template <int NT>
+__device__ __forceinline__ TileLoc find_tile(const MatmulParams& p, int32_t tile_rows,
+                                             int32_t* sh) {
+  TileLoc loc;
+  int32_t rt;
+  if (!p.grouped) {
+    tile_of(blockIdx.x, (uint32_t)p.row_tiles, (uint32_t)p.col_tiles, &rt, &loc.col);
+    loc.e = 0;
+    loc.row = rt < 0 ? -1 : rt * tile_rows;
+    const int64_t e = (int64_t)loc.row + tile_rows;
+    loc.end = (int32_t)(e < p.T ? e : p.T);
+    return loc;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int32_t per = (p.batches + NT - 1) / NT;
+  const int32_t b0 = tid * per, b1 = b0 + per < p.batches ? b0 + per : p.batches;
+  int32_t row = 0, end = 0, e = 0, mine = 0;
+  for (int32_t b = b0; b < b1; ++b) mine += read_group(p, b, tile_rows, &row, &end, &e);
+  const int32_t incl = wave_inclusive_sum(mine);
+  if (lane == 63) sh[wave] = incl;
+  __syncthreads();
+  int32_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) {
+    before += w < wave ? sh[w] : 0;
+    total += sh[w];
+  }
+  total = uniform(total);
+  tile_of(blockIdx.x, (uint32_t)total, (uint32_t)p.col_tiles, &rt, &loc.col);
+  loc.row = -1;
+  loc.end = loc.e = 0;
+  if (rt < 0) return loc;  // the same in every thread of the workgroup
+  int32_t at = before + incl - mine;
+  if (rt >= at && rt < at + mine) {
+    for (int32_t b = b0; b < b1; ++b) {
+      const int32_t n = read_group(p, b, tile_rows, &row, &end, &e);
+      if (rt < at + n) {
+        const int32_t r = row + (rt - at) * tile_rows;
+        sh[NT / 64] = r;
+        sh[NT / 64 + 1] = end - r > tile_rows ? r + tile_rows : end;
+        sh[NT / 64 + 2] = e;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  loc.row = uniform(sh[NT / 64]);
+  loc.end = uniform(sh[NT / 64 + 1]);
+  loc.e = uniform(sh[NT / 64 + 2]);
+  return loc;
+}
+
+// ---------------------------------------------------------------------------
+// Adapters of a tile's rows.
+// ---------------------------------------------------------------------------
+
+// Fill row_a[0 .. ROWS) with the adapter of rows row0 + i (-1: none) and
+// list[0 .. *count) with the distinct ones, in order of their first row (all
+// NT threads take part; NT >= ROWS; `count` is a word of LDS).  Segments are
+// disjoint, so every row is written by one thread at most.
+template <int NT, int ROWS>
+__device__ __forceinline__ void tile_adapters(const MatmulParams& p, int32_t row0, int32_t end,
+                                              int32_t* row_a, int32_t* list, int32_t* count) {
+  static_assert(NT >= ROWS && ROWS % 64 == 0, "one row per thread");
+  const int tid = threadIdx.x;
+  if (tid < ROWS) row_a[tid] = -1;
+  if (tid == 0) *count = 0;
+  __syncthreads();
+  for (int32_t b = tid; b < p.batches; b += NT) {
+    const int64_t st = p.start[b], ln = p.lens[b], a = p.idx[b];
+    if (a < 0 || a >= p.L || ln <= 0 || st < 0 || st > p.T - ln) continue;
+    const int64_t lo = st > row0 ? st : row0, hi = st + ln < end ? st + ln : end;
+    for (int64_t r = lo; r < hi; ++r) row_a[r - row0] = (int32_t)a;
+  }
+  __syncthreads();
+  // A row is listed when no earlier row has its adapter.
+  bool first = false;
+  int32_t mine = -1;
+  if (tid < ROWS) {
+    mine = row_a[tid];
+    first = mine >= 0;
+    for (int i = 0; i < ROWS; i += 4) {
+      const int4 q = *reinterpret_cast<const int4*>(row_a + i);
+      first = first && !((q.x == mine && i < tid) || (q.y == mine && i + 1 < tid) ||
+                         (q.z == mine && i + 2 < tid) || (q.w == mine && i + 3 < tid));
+    }
+  }
+  const uint64_t m = __ballot(first);
+  const int lane = tid & 63;
+  const int before = __builtin_popcountll(m & ((1ull << lane) - 1));
+#pragma unroll
+  for (int w = 0; w < ROWS / 64; ++w) {  // wave after wave, so that the order is the rows'
+    if (tid >> 6 == w) {
+      const int32_t at = *count;
+      if (first) list[at + before] = mine;
+      if (lane == 0) *count = at + __builtin_popcountll(m);
+    }
+    __syncthreads();
+  }
+}
+
+// Eight float32 values as two packed operands of the 16-bit weight dtype,
+// v = hi + lo to 16 (bfloat16) or 22 (float16) bits: one rounding to the
+// weights' dtype would leave the adapters' share of a float32 result with an
+// error of 2^-9 or 2^-12.  A value past float16's range becomes an infinity.
+template <int WD>
+__device__ __forceinline__ void split_operand(const float* v, u32x4* hi, u32x4* lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = pack2<WD>(v[2 * i], v[2 * i + 1]);
+    const float h0 = widen<WD>(h & 0xFFFFu), h1 = widen<WD>(h >> 16);
+    // the rest of an infinity is nothing (inf - inf would be NaN)
+    const float r0 = __builtin_isinf(h0) ? 0.f : v[2 * i] - h0;
+    const float r1 = __builtin_isinf(h1) ? 0.f : v[2 * i + 1] - h1;
+    (*hi)[i] = h;
+    (*lo)[i] = pack2<WD>(r0, r1);
+  }
+}
+
+// silu(g) * u = g u / (1 + exp(-g)).  For g -> -inf exp overflows to +inf and
+// the quotient is -0; g = -inf itself gives NaN, as -inf * 0 does.
+__device__ __forceinline__ float gate(float g, float u) {
+  return g / (1.f + __expf(-g)) * u;
+}
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
+  if (dtype == F32) return static_cast<const float*>(p)[i];
+  const uint32_t h = static_cast<const uint16_t*>(p)[i];
+  return dtype == BF16 ? widen<BF16>(h) : widen<F16>(h);
+}
+
+__device__ __forceinline__ void store_elem(void* p, int64_t i, int dtype, float v) {
+  if (dtype == F32) {
+    static_cast<float*>(p)[i] = v;
+  } else {
+    const uint32_t h = dtype == BF16 ? pack2<BF16>(v, 0.f) : pack2<F16>(v, 0.f);
+    static_cast<uint16_t*>(p)[i] = (uint16_t)h;
+  }
+}
+
+}  // namespace dev
+}  // namespace sgmv

@@ -1,0 +1,278 @@
+// sgmv_matmul_api.cpp -- libsgmv C entry points of the shared projection
+// with the adapters of many requests (sgmv_lora_linear) and of the products
+// grouped by expert (sgmv_grouped_gemm): argument checks, kernel choice, grid
+// sizing and launch.  No allocation, no synchronisation, no device-to-host
+// traffic.
+#include <stdint.h>
+
+#include "sgmv.h"
+#include "sgmv_host.h"
+#include "sgmv_limits.h"
+#include "sgmv_matmul_launch.h"
+
+namespace {
+
+using namespace sgmv::host;
+
+sgmv_status check_inputs(const sgmv_matrix& x, const sgmv_matrix& out) {
+  if (!known_dtype(x.dtype)) return fail(SGMV_ERR_INVALID_ARGUMENT, "unknown inputs dtype %d", x.dtype);
+  if (!known_dtype(out.dtype)) return fail(SGMV_ERR_INVALID_ARGUMENT, "unknown output dtype %d", out.dtype);
+  if (x.rows < 0 || x.cols < 1 || x.row_stride < x.cols)
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "inputs shape (%lld, %lld) with row stride %lld is invalid", (long long)x.rows,
+                (long long)x.cols, (long long)x.row_stride);
+  if (out.rows < 0 || out.cols < 0 || out.row_stride < out.cols)
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "output shape (%lld, %lld) with row stride %lld is invalid", (long long)out.rows,
+                (long long)out.cols, (long long)out.row_stride);
+  if (x.rows > INT32_MAX || out.rows > INT32_MAX)
+    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^31-1 rows");
+  if (x.cols > INT32_MAX - 4096 || out.cols > INT32_MAX / 2 - 4096)
+    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^31-1 columns");
+  return SGMV_OK;
+}
+
+sgmv_status check_segments(int64_t batches, int64_t max_seq_len) {
+  if (batches < 0) return fail(SGMV_ERR_INVALID_ARGUMENT, "batches must be >= 0");
+  if (batches > SGMV_MAX_BATCHES)
+    return fail(SGMV_ERR_UNSUPPORTED, "batches %lld exceeds %d", (long long)batches,
+                SGMV_MAX_BATCHES);
+  if (max_seq_len < 0) return fail(SGMV_ERR_INVALID_ARGUMENT, "max_seq_len must be >= 0");
+  return SGMV_OK;
+}
+
+// Launches `kernel` on row tiles x column tiles of rows x cols.
+sgmv_status launch(const void* kernel, sgmv::MatmulParams& p, int rows, int cols, int threads,
+                   hipStream_t stream) {
+  if (!kernel) return fail(SGMV_ERR_UNSUPPORTED, "no kernel for this dtype combination");
+  // Grouped: at most ceil(T / rows) + min(batches, T) tiles.
+  int64_t row_tiles = (p.T + rows - 1) / rows;
+  if (p.grouped) row_tiles += p.batches < p.T ? p.batches : p.T;
+  const int64_t col_tiles = ((int64_t)p.N + cols - 1) / cols;
+  if (row_tiles * col_tiles > INT32_MAX)
+    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^31-1 work units");
+  p.row_tiles = (int32_t)row_tiles;
+  p.col_tiles = (int32_t)col_tiles;
+  void* args[] = {&p};
+  const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)(row_tiles * col_tiles)),
+                                       dim3((unsigned)threads), args, 0, stream);
+  if (e != hipSuccess) return fail(SGMV_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  return SGMV_OK;
+}
+
+// The kernel for p's sizes, types and alignment.
+sgmv_status run(sgmv::MatmulParams& p, int wd, bool gated, hipStream_t stream) {
+  using namespace sgmv;
+  return launch(matmul_generic_kernel(wd, gated), p, kGenericRows, kGenericCols, kThreads, stream);
+}
+
+// Row stride (floats) of the projected rows of one slice in the workspace:
+// whole 32-byte blocks, as the projection's vector stores want them.
+int64_t projected_stride(int64_t rank) { return (rank + 7) / 8 * 8; }
+int64_t projected_bytes(int64_t tokens, int64_t rank) {
+  return (tokens * projected_stride(rank) * 4 + 255) / 256 * 256;
+}
+
+}  // namespace
+
+extern "C" {
+
+sgmv_status sgmv_lora_linear_workspace_bytes(int64_t tokens, int num_slices, int64_t rank,
+                                             size_t* bytes) {
+  if (!bytes) return fail(SGMV_ERR_INVALID_ARGUMENT, "bytes pointer is null");
+  if (tokens < 0 || num_slices < 0 || num_slices > SGMV_MAX_SLICES || rank < 0)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "tokens, num_slices (<= %d) and rank must be >= 0",
+                SGMV_MAX_SLICES);
+  if (tokens > INT32_MAX || rank > SGMV_MAX_RANK)
+    return fail(SGMV_ERR_UNSUPPORTED, "tokens exceed 2^31-1 or the rank %d", SGMV_MAX_RANK);
+  *bytes = (size_t)(num_slices * projected_bytes(tokens, rank));
+  g_error.clear();
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void* bias,
+                             const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
+                             const int64_t* b_seq_start_loc, const int64_t* seq_lens,
+                             const int64_t* lora_indices, int64_t batches, int64_t max_seq_len,
+                             float scale, int add_inputs, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+  using namespace sgmv;
+  if (num_slices < 0 || num_slices > SGMV_MAX_SLICES)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "num_slices must be in 0..%d, got %d", SGMV_MAX_SLICES,
+                num_slices);
+  if (num_slices > 0 && !slices) return fail(SGMV_ERR_INVALID_ARGUMENT, "slices pointer is null");
+  const sgmv_matrix& x = inputs;
+  sgmv_status st = check_inputs(x, out);
+  if (st != SGMV_OK) return st;
+  if (out.rows != x.rows)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "output must have the inputs' %lld rows",
+                (long long)x.rows);
+  if (!known_dtype(weight.dtype))
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "unknown weight dtype %d", weight.dtype);
+  if (weight.dtype == SGMV_F32 || x.dtype != weight.dtype)
+    return fail(SGMV_ERR_UNSUPPORTED, "inputs and weight must share one 16-bit dtype");
+  if (weight.cols != x.cols || weight.rows != out.cols || weight.row_stride < weight.cols)
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "weight (%lld, %lld) with row stride %lld must be (output columns %lld, hidden %lld)",
+                (long long)weight.rows, (long long)weight.cols, (long long)weight.row_stride,
+                (long long)out.cols, (long long)x.cols);
+  st = check_segments(batches, max_seq_len);
+  if (st != SGMV_OK) return st;
+
+  int64_t K = 0, L = 0;
+  for (int i = 0; i < num_slices; ++i) {
+    const sgmv_fused_slice& s = slices[i];
+    if (!known_dtype(s.lora_a.dtype) || !known_dtype(s.lora_b.dtype))
+      return fail(SGMV_ERR_INVALID_ARGUMENT, "slice %d: unknown dtype", i);
+    if (s.lora_a.dtype != weight.dtype || s.lora_b.dtype != weight.dtype)
+      return fail(SGMV_ERR_UNSUPPORTED, "slice %d: lora_a and lora_b must have the weight's dtype",
+                  i);
+    if (s.lora_a.num < 0 || s.lora_a.rows < 1 || s.lora_a.cols != x.cols)
+      return fail(SGMV_ERR_INVALID_ARGUMENT, "slice %d: lora_a must be (lora_num, rank, %lld)", i,
+                  (long long)x.cols);
+    if (s.lora_b.num != s.lora_a.num || s.lora_b.cols != s.lora_a.rows || s.lora_b.rows < 0)
+      return fail(SGMV_ERR_INVALID_ARGUMENT,
+                  "slice %d: lora_b must be (lora_num, slice_size, rank) with lora_a's "
+                  "lora_num and rank", i);
+    if (s.slice_offset < 0 || s.slice_offset > out.cols - s.lora_b.rows)
+      return fail(SGMV_ERR_INVALID_ARGUMENT,
+                  "slice %d: window [%lld, %lld) is outside the %lld output columns", i,
+                  (long long)s.slice_offset, (long long)(s.slice_offset + s.lora_b.rows),
+                  (long long)out.cols);
+    if (i == 0) {
+      K = s.lora_a.rows;
+      L = s.lora_a.num;
+    } else if (s.lora_a.rows != K || s.lora_a.num != L) {
+      return fail(SGMV_ERR_INVALID_ARGUMENT, "slice %d: rank and lora_num must match slice 0", i);
+    }
+    for (int q = 0; q < i; ++q) {
+      const sgmv_fused_slice& o = slices[q];
+      if (s.lora_b.rows > 0 && o.lora_b.rows > 0 &&
+          s.slice_offset < o.slice_offset + o.lora_b.rows &&
+          o.slice_offset < s.slice_offset + s.lora_b.rows)
+        return fail(SGMV_ERR_INVALID_ARGUMENT, "slices %d and %d overlap", q, i);
+    }
+  }
+  if (L > INT32_MAX) return fail(SGMV_ERR_UNSUPPORTED, "lora_num exceeds 2^31-1");
+  if (K > SGMV_MAX_RANK)
+    return fail(SGMV_ERR_UNSUPPORTED, "rank %lld exceeds %d", (long long)K, SGMV_MAX_RANK);
+  if (x.rows == 0 || out.cols == 0) {
+    g_error.clear();
+    return SGMV_OK;  // nothing to do
+  }
+  if (!x.data || !out.data || !weight.data)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "null data pointer");
+  const bool adapters = num_slices > 0 && batches > 0 && L > 0;
+  if (adapters) {
+    if (!b_seq_start_loc || !seq_lens || !lora_indices)
+      return fail(SGMV_ERR_INVALID_ARGUMENT, "segment metadata pointer is null");
+    for (int i = 0; i < num_slices; ++i)
+      if (!slices[i].lora_a.data || (slices[i].lora_b.rows > 0 && !slices[i].lora_b.data))
+        return fail(SGMV_ERR_INVALID_ARGUMENT, "slice %d: null data pointer", i);
+    const size_t need = (size_t)(num_slices * projected_bytes(x.rows, K));
+    if (!workspace || workspace_bytes < need || !aligned16(workspace))
+      return fail(SGMV_ERR_INVALID_ARGUMENT,
+                  "workspace must be 16-byte aligned and hold %zu bytes, got %zu", need,
+                  workspace ? workspace_bytes : (size_t)0);
+  }
+
+  MatmulParams p{};
+  p.x = x.data;
+  p.w = weight.data;
+  p.bias = bias;
+  p.out = out.data;
+  p.x_row_bytes = x.row_stride * 2;
+  p.w_row_bytes = weight.row_stride * 2;
+  p.out_row_bytes = out.row_stride * elem_bytes(out.dtype);
+  p.T = p.X = x.rows;
+  p.H = (int32_t)x.cols;
+  p.N = (int32_t)out.cols;
+  p.out_dtype = out.dtype;
+  p.add = add_inputs != 0;
+  if (adapters) {
+    // First the projections onto the adapters' rank, kept in float32.
+    sgmv_shrink_slice down[SGMV_MAX_SLICES];
+    p.start = b_seq_start_loc;
+    p.lens = seq_lens;
+    p.idx = lora_indices;
+    p.batches = (int32_t)batches;
+    p.L = (int32_t)L;
+    p.num_slices = num_slices;
+    p.K = (int32_t)K;
+    p.v_stride = (int32_t)projected_stride(K);
+    for (int i = 0; i < num_slices; ++i) {
+      float* v = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                          i * projected_bytes(x.rows, K));
+      down[i].lora_a = slices[i].lora_a;
+      down[i].out = sgmv_matrix{v, SGMV_F32, x.rows, K, p.v_stride};
+      p.s[i] = AdapterDesc{slices[i].lora_b.data, v, slices[i].lora_b.rows, slices[i].slice_offset};
+    }
+    st = sgmv_shrink_multi_slice(inputs, down, num_slices, b_seq_start_loc, seq_lens, lora_indices,
+                                 batches, max_seq_len, scale, nullptr, 0, stream);
+    if (st != SGMV_OK) return st;
+  }
+  st = run(p, weight.dtype, false, stream);
+  if (st == SGMV_OK) g_error.clear();
+  return st;
+}
+
+sgmv_status sgmv_grouped_gemm(sgmv_matrix inputs, sgmv_stack weights, sgmv_matrix out,
+                              const int64_t* row_indices, const int64_t* b_seq_start_loc,
+                              const int64_t* seq_lens, const int64_t* expert_indices,
+                              int64_t batches, int64_t max_seq_len, int gated,
+                              hipStream_t stream) {
+  using namespace sgmv;
+  const sgmv_matrix& x = inputs;
+  sgmv_status st = check_inputs(x, out);
+  if (st != SGMV_OK) return st;
+  if (!known_dtype(weights.dtype))
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "unknown weights dtype %d", weights.dtype);
+  if (weights.dtype == SGMV_F32 || x.dtype != weights.dtype)
+    return fail(SGMV_ERR_UNSUPPORTED, "inputs and weights must share one 16-bit dtype");
+  if (weights.num < 0 || weights.cols != x.cols ||
+      weights.rows != (gated ? 2 * out.cols : out.cols))
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "weights must be (experts, %lld, %lld), got (%lld, %lld, %lld)",
+                (long long)(gated ? 2 * out.cols : out.cols), (long long)x.cols,
+                (long long)weights.num, (long long)weights.rows, (long long)weights.cols);
+  if (!row_indices && x.rows != out.rows)
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "output must have the inputs' %lld rows without row_indices", (long long)x.rows);
+  if (weights.num > INT32_MAX) return fail(SGMV_ERR_UNSUPPORTED, "experts exceed 2^31-1");
+  st = check_segments(batches, max_seq_len);
+  if (st != SGMV_OK) return st;
+  if (batches == 0 || out.rows == 0 || out.cols == 0 || weights.num == 0) {
+    g_error.clear();
+    return SGMV_OK;  // nothing to do
+  }
+  if ((!x.data && x.rows > 0) || !out.data || !weights.data)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "null data pointer");
+  if (!b_seq_start_loc || !seq_lens)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "segment metadata pointer is null");
+
+  MatmulParams p{};
+  p.x = x.data;
+  p.w = weights.data;
+  p.out = out.data;
+  p.start = b_seq_start_loc;
+  p.lens = seq_lens;
+  p.idx = expert_indices;
+  p.rows = row_indices;
+  p.x_row_bytes = x.row_stride * 2;
+  p.w_row_bytes = weights.cols * 2;
+  p.w_mat_bytes = weights.rows * weights.cols * 2;
+  p.out_row_bytes = out.row_stride * elem_bytes(out.dtype);
+  p.T = out.rows;
+  p.X = x.rows;
+  p.H = (int32_t)x.cols;
+  p.N = (int32_t)out.cols;
+  p.batches = (int32_t)batches;
+  p.L = (int32_t)weights.num;
+  p.grouped = 1;
+  p.out_dtype = out.dtype;
+  st = run(p, weights.dtype, gated != 0, stream);
+  if (st == SGMV_OK) g_error.clear();
+  return st;
+}
+
+}  // extern "C"

@@ -1,0 +1,228 @@
+"""The shared projection with adapters and the grouped products on the GPU,
+against their plain 64-bit forms (matmul_util)."""
+import numpy as np
+import pytest
+import torch
+
+import matmul_util as U
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def normal(gen, *shape, sigma=1.0, dtype=BF16):
+    return (torch.randn(*shape, generator=gen) * sigma).to(dtype).cuda()
+
+
+def i64(v):
+    return torch.tensor(v, dtype=torch.int64, device="cuda")
+
+
+def guarded(T, N, dtype, pad=0, gen=None):
+    """An output of N columns inside wider rows, all set to a known value."""
+    full = torch.full((T, N + pad), 7.0, dtype=dtype, device="cuda")
+    if gen is not None:
+        full[:, :N] = torch.randn(T, N, generator=gen).to(dtype).cuda()
+    return full, full[:, :N]
+
+
+def lora_case(T, H, widths, K, L, lens, idx, dtype=BF16, out=None, bias=False, add=False, scale=0.5,
+              start=None, seed=0, pad_x=0, pad_out=0, gaps=()):
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(seed)
+    N = sum(widths) + sum(gaps)
+    out = out or dtype
+    x = normal(gen, T, H + pad_x, dtype=dtype)[:, :H]
+    w = normal(gen, N, H, sigma=H ** -0.5, dtype=dtype)
+    b = normal(gen, N, dtype=dtype) if bias else None
+    slices, at = [], 0
+    for i, n in enumerate(widths):
+        slices.append((normal(gen, L, K, H, sigma=H ** -0.5, dtype=dtype),
+                       normal(gen, L, n, K, sigma=0.3, dtype=dtype), at))
+        at += n + (gaps[i] if i < len(gaps) else 0)
+    if start is None:
+        start = np.concatenate([[0], np.cumsum(lens)[:-1]]).astype(int).tolist() if lens else []
+    full, o = guarded(T, N, out, pad_out, gen)
+    o0 = o.clone()
+    print(f"lora_linear T={T} H={H} N={N} K={K} L={L} segments={len(lens)} {dtype}->{out}", flush=True)
+    sg.sgmv_lora_linear(x, w, slices, o, i64(start), i64(lens), i64(idx), len(lens),
+                        max(lens, default=0), scaling=scale, bias=b, add_inputs=add)
+    torch.cuda.synchronize()
+    want, bound = U.lora_linear(x, w, b, slices, start, lens, idx, scale, o0, add, out)
+    U.assert_within(o, want, bound)
+    assert pad_out == 0 or bool((full[:, N:] == 7.0).all())
+
+
+# Sizes around the tiles' edges (16, 64, 128 and 256 rows and columns, 64-wide steps), one token
+# to several tiles.
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 33, 64, 65, 127, 130, 257, 520])
+def test_lora_linear_rows(T):
+    half = max(1, T // 2)
+    lens = [half, T - half] if T > 1 else [1]
+    lora_case(T, 256, [320], 16, 3, lens, [2, -1][:len(lens)] if T % 2 else [1, 2][:len(lens)], seed=T)
+
+
+@pytest.mark.parametrize("H", [8, 24, 32, 64, 72, 136, 200, 512, 1032])
+@pytest.mark.parametrize("T", [5, 150])
+def test_lora_linear_hidden(T, H):
+    lora_case(T, H, [128], 8, 2, [T], [1], dtype=F16, seed=H)
+
+
+@pytest.mark.parametrize("widths", [[8], [16], [24], [72], [128, 64, 64], [264], [520], [40, 8, 136]])
+@pytest.mark.parametrize("T", [3, 140, 300])
+def test_lora_linear_widths(T, widths):
+    lora_case(T, 192, widths, 16, 4, [T - 2, 2], [3, 0], bias=True, seed=sum(widths))
+
+
+@pytest.mark.parametrize("K", [1, 8, 13, 16, 24, 32, 64, 100, 128, 256])
+@pytest.mark.parametrize("T", [4, 200])
+def test_lora_linear_ranks(T, K):
+    lora_case(T, 320, [192], K, 3, [T // 2, T // 2], [0, 2], seed=K)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("out", [BF16, F16, F32])
+@pytest.mark.parametrize("T,add", [(7, False), (7, True), (190, False), (190, True), (400, True)])
+def test_lora_linear_types(dtype, out, T, add):
+    lora_case(T, 264, [136, 200], 24, 3, [T - 3, 3], [1, 2], dtype=dtype, out=out, bias=True, add=add)
+
+
+@pytest.mark.parametrize("T,H,N,pad_x,pad_out", [(9, 130, 67, 3, 5), (150, 130, 67, 3, 5), (9, 128, 66, 0, 1),
+                                                 (300, 66, 131, 8, 0), (70, 7, 1, 1, 0), (1, 1, 1, 0, 0)])
+def test_lora_linear_odd_sizes_and_strides(T, H, N, pad_x, pad_out):
+    lora_case(T, H, [N], 5, 2, [T], [1], pad_x=pad_x, pad_out=pad_out, bias=True)
+
+
+@pytest.mark.parametrize("T", [40, 64, 300, 513])
+def test_lora_linear_many_adapters(T):
+    """One token a segment, many adapters inside every tile, some rows without one."""
+    rng = np.random.default_rng(T)
+    lora_case(T, 256, [256, 64], 16, 24, [1] * T, rng.integers(-1, 24, T).tolist(), seed=T)
+
+
+@pytest.mark.parametrize("T", [50, 300])
+def test_lora_linear_segment_layouts(T):
+    """Unsorted starts, gaps, empty segments, and segments that break a precondition: those get the
+    shared projection alone."""
+    start = [T - 10, 5, 20, 0, 12, T - 1, -1, 30, 30]
+    lens = [10, 4, 0, 3, 6, 2, 3, 5, -2]
+    idx = [1, 0, 1, 2, -1, 1, 1, 7, 1]
+    lora_case(T, 128, [192], 16, 3, lens, idx, start=start)
+
+
+@pytest.mark.parametrize("T", [6, 210])
+def test_lora_linear_without_adapters(T):
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T)
+    x, w = normal(gen, T, 256), normal(gen, 192, 256, sigma=1 / 16)
+    o = torch.empty(T, 192, dtype=F32, device="cuda")
+    none = i64([])
+    sg.sgmv_lora_linear(x, w, [], o, none, none, none, 0, 0)
+    want, bound = U.lora_linear(x, w, None, [], [], [], [], 1.0, o, False, F32)
+    U.assert_within(o, want, bound)
+
+
+@pytest.mark.parametrize("T", [20, 280])
+def test_lora_linear_windows_with_gaps(T):
+    """Columns between and after the slices' windows get the shared projection alone."""
+    lora_case(T, 136, [40, 24], 8, 2, [T], [1], gaps=(72, 104), seed=T)
+
+
+@pytest.mark.parametrize("T", [12, 260])
+def test_lora_linear_nan_rows_stay_where_they_are(T):
+    """NaN and infinities of one row reach that row alone; rows of the workspace that no segment
+    wrote are never used."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(1)
+    H, N, K, L = 200, 144, 16, 2
+    x, w = normal(gen, T, H), normal(gen, N, H, sigma=H ** -0.5)
+    la, lb = normal(gen, L, K, H, sigma=H ** -0.5), normal(gen, L, N, K)
+    bad = [3, T - 1]
+    x[3, 5], x[T - 1, H - 1] = float("nan"), float("inf")
+    ws = torch.full((sg.lora_linear_workspace_bytes(T, 1, K),), 255, dtype=torch.uint8, device="cuda")
+    o = torch.zeros(T, N, dtype=BF16, device="cuda")
+    start, lens, idx = [0, 6], [5, T - 8], [1, -1]
+    sg.sgmv_lora_linear(x, w, [(la, lb, 0)], o, i64(start), i64(lens), i64(idx), 2, T, workspace=ws)
+    keep = [t for t in range(T) if t not in bad]
+    want, bound = U.lora_linear(x, w, None, [(la, lb, 0)], start, lens, idx, 1.0, o, False, BF16)
+    U.assert_within(o[keep], want[keep], bound[keep])
+    assert not torch.isfinite(o[bad].float()).any()
+
+
+def grouped_case(lens, H, N, E=None, idx=None, rows=None, X=None, gated=False, dtype=BF16, out=None,
+                 start=None, T=None, seed=0, pad_x=0, pad_out=0):
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(seed)
+    E = E or len(lens)
+    if start is None:
+        start = np.concatenate([[0], np.cumsum(lens)[:-1]]).astype(int).tolist()
+    T = sum(lens) if T is None else T
+    X = T if X is None else X
+    x = normal(gen, X, H + pad_x, dtype=dtype)[:, :H]
+    w = normal(gen, E, 2 * N if gated else N, H, sigma=2 * H ** -0.5, dtype=dtype)
+    full, o = guarded(T, N, out or dtype, pad_out, gen)
+    o0 = o.clone()
+    print(f"grouped_gemm T={T} H={H} N={N} E={E} gated={gated} {dtype}->{o.dtype}", flush=True)
+    sg.sgmv_grouped_gemm(x, w, o, i64(start), i64(lens), None if idx is None else i64(idx), len(lens),
+                         max(lens), row_indices_tensor=None if rows is None else i64(rows), gated=gated)
+    torch.cuda.synchronize()
+    want, bound, written = U.grouped(x, w, start, lens, idx, rows, gated, o0)
+    U.assert_within(o[written.cuda()], want[written], bound[written])
+    assert torch.equal(o[~written.cuda()], o0[~written.cuda()])
+    assert pad_out == 0 or bool((full[:, N:] == 7.0).all())
+
+
+LENS = [[1], [0, 1, 0, 2], [16, 17, 15, 64, 65], [3, 300, 0, 129, 1], [1] * 40, [255, 256, 257],
+        [600, 0, 0, 5]]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("lens", LENS)
+def test_grouped_rows(lens, gated):
+    grouped_case(lens, 192, 160, gated=gated, seed=len(lens))
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("H,N", [(8, 8), (64, 24), (72, 136), (200, 40), (328, 264), (1032, 72)])
+@pytest.mark.parametrize("lens", [[2, 0, 5], [70, 130, 300]])
+def test_grouped_sizes(lens, H, N, gated):
+    grouped_case(lens, H, N, gated=gated, dtype=F16, seed=H)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("out", [BF16, F16, F32])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("lens", [[4, 1, 9], [140, 30, 200]])
+def test_grouped_types(dtype, out, gated, lens):
+    grouped_case(lens, 136, 152, dtype=dtype, out=out, gated=gated)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("lens", [[4, 1, 9], [140, 30, 200], [300, 100, 270]])
+def test_grouped_gathered_rows(lens, gated):
+    """Rows picked from fewer inputs, repeated and in any order; an index outside the inputs is a row
+    of zeros."""
+    rng = np.random.default_rng(3)
+    T = sum(lens)
+    rows = rng.integers(0, 37, T)
+    rows[[1, T - 1]] = [-1, 37]
+    grouped_case(lens, 264, 136, rows=rows.tolist(), X=37, gated=gated)
+
+
+@pytest.mark.parametrize("T", [60, 400])
+def test_grouped_segment_layouts(T):
+    """Unsorted starts, gaps, repeated and missing experts; rows outside the segments stay."""
+    grouped_case([10, 0, T // 2, 3, 5, 6, -1], 128, 96, E=3, idx=[2, 1, 2, -1, 0, 3, 1],
+                 start=[T - 10, 4, 8, 0, 3, T - 20, 2], T=T)
+
+
+@pytest.mark.parametrize("H,N,pad_x,pad_out", [(129, 67, 2, 3), (66, 9, 6, 1), (5, 3, 0, 0), (64, 33, 0, 0)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_odd_sizes_and_strides(H, N, pad_x, pad_out, gated):
+    grouped_case([3, 90, 0, 20], H, N, gated=gated, pad_x=pad_x, pad_out=pad_out)
+
+
+def test_grouped_many_segments():
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 3, 900)
+    grouped_case(lens.tolist(), 64, 32, E=5, idx=rng.integers(-1, 5, 900).tolist())
