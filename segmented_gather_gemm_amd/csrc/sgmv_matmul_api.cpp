@@ -41,29 +41,54 @@ sgmv_status check_segments(int64_t batches, int64_t max_seq_len) {
   return SGMV_OK;
 }
 
-// Launches `kernel` on row tiles x column tiles of rows x cols.
-sgmv_status launch(const void* kernel, sgmv::MatmulParams& p, int rows, int cols, int threads,
-                   hipStream_t stream) {
-  if (!kernel) return fail(SGMV_ERR_UNSUPPORTED, "no kernel for this dtype combination");
-  // Grouped: at most ceil(T / rows) + min(batches, T) tiles.
-  int64_t row_tiles = (p.T + rows - 1) / rows;
-  if (p.grouped) row_tiles += p.batches < p.T ? p.batches : p.T;
-  const int64_t col_tiles = ((int64_t)p.N + cols - 1) / cols;
-  if (row_tiles * col_tiles > INT32_MAX)
+// The kernel that p's sizes, types and alignment take, its tile and its grid.
+struct Plan {
+  const void* kernel;
+  int rows, cols, threads;
+  int64_t row_tiles, col_tiles;
+};
+
+int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
+
+// Whether the tiled kernels' 16-byte blocks and 32-bit offsets fit: hidden a
+// multiple of eight, aligned rows, and less than 2 GiB from the first to the
+// last row of a tile (gathered: of the inputs).
+bool tiled_fits(const sgmv::MatmulParams& p) {
+  const int64_t most = int64_t(1) << 31, rows = 256;
+  return p.H % 8 == 0 && aligned16(p.x) && aligned16(p.w) && p.x_row_bytes % 16 == 0 &&
+         p.w_row_bytes % 16 == 0 && p.w_mat_bytes % 16 == 0 && rows * p.w_row_bytes < most &&
+         (p.rows ? p.X : rows) * p.x_row_bytes < most;
+}
+
+sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan) {
+  using namespace sgmv;
+  const int mode = gated ? 2 : p.grouped ? 1 : 0;
+  if (tiled_fits(p)) {
+    const TiledKernel k = matmul_tiled_large(wd, mode);
+    *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0};
+  } else {
+    *plan = Plan{matmul_generic_kernel(wd, gated), kGenericRows, kGenericCols, kThreads, 0, 0};
+  }
+  if (!plan->kernel) return fail(SGMV_ERR_UNSUPPORTED, "no kernel for this dtype combination");
+  // Grouped: at most ceil(T / rows) + min(batches, T) row tiles.
+  plan->row_tiles = tiles(p.T, plan->rows) + (p.grouped ? (p.batches < p.T ? p.batches : p.T) : 0);
+  plan->col_tiles = tiles(p.N, plan->cols);
+  if (plan->row_tiles * plan->col_tiles > INT32_MAX)
     return fail(SGMV_ERR_UNSUPPORTED, "more than 2^31-1 work units");
-  p.row_tiles = (int32_t)row_tiles;
-  p.col_tiles = (int32_t)col_tiles;
-  void* args[] = {&p};
-  const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)(row_tiles * col_tiles)),
-                                       dim3((unsigned)threads), args, 0, stream);
-  if (e != hipSuccess) return fail(SGMV_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   return SGMV_OK;
 }
 
-// The kernel for p's sizes, types and alignment.
-sgmv_status run(sgmv::MatmulParams& p, int wd, bool gated, hipStream_t stream) {
-  using namespace sgmv;
-  return launch(matmul_generic_kernel(wd, gated), p, kGenericRows, kGenericCols, kThreads, stream);
+sgmv_status launch(const Plan& plan, sgmv::MatmulParams& p, hipStream_t stream) {
+  p.row_tiles = (int32_t)plan.row_tiles;
+  p.col_tiles = (int32_t)plan.col_tiles;
+  p.vec_out = aligned16(p.out) && p.out_row_bytes % 16 == 0;
+  p.vec_bias = aligned16(p.bias);
+  void* args[] = {&p};
+  const hipError_t e = hipLaunchKernel(plan.kernel, dim3((unsigned)(plan.row_tiles * plan.col_tiles)),
+                                       dim3((unsigned)plan.threads), args, 0, stream);
+  if (e != hipSuccess) return fail(SGMV_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  g_error.clear();
+  return SGMV_OK;
 }
 
 // Row stride (floats) of the projected rows of one slice in the workspace:
@@ -189,6 +214,9 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
   p.N = (int32_t)out.cols;
   p.out_dtype = out.dtype;
   p.add = add_inputs != 0;
+  Plan plan;
+  st = make_plan(p, weight.dtype, false, &plan);
+  if (st != SGMV_OK) return st;
   if (adapters) {
     // First the projections onto the adapters' rank, kept in float32.
     sgmv_shrink_slice down[SGMV_MAX_SLICES];
@@ -211,9 +239,7 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
                                  batches, max_seq_len, scale, nullptr, 0, stream);
     if (st != SGMV_OK) return st;
   }
-  st = run(p, weight.dtype, false, stream);
-  if (st == SGMV_OK) g_error.clear();
-  return st;
+  return launch(plan, p, stream);
 }
 
 sgmv_status sgmv_grouped_gemm(sgmv_matrix inputs, sgmv_stack weights, sgmv_matrix out,
@@ -270,9 +296,10 @@ sgmv_status sgmv_grouped_gemm(sgmv_matrix inputs, sgmv_stack weights, sgmv_matri
   p.L = (int32_t)weights.num;
   p.grouped = 1;
   p.out_dtype = out.dtype;
-  st = run(p, weights.dtype, gated != 0, stream);
-  if (st == SGMV_OK) g_error.clear();
-  return st;
+  Plan plan;
+  st = make_plan(p, weights.dtype, gated != 0, &plan);
+  if (st != SGMV_OK) return st;
+  return launch(plan, p, stream);
 }
 
 }  // extern "C"

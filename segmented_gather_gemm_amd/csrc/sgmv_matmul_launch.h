@@ -43,6 +43,8 @@ struct MatmulParams {
   int32_t grouped;
   int32_t out_dtype;
   int32_t add;            // dense: accumulate onto out
+  int32_t vec_out;        // 16-byte accesses of eight columns of out are legal
+  int32_t vec_bias;       // ... of eight values of bias
   int32_t col_tiles;      // column tiles of the launch
   int32_t row_tiles;      // dense: row tiles; grouped: bound on them (the device counts)
   int32_t num_slices;     // adapters: slices, rank, v's row stride (floats)
@@ -54,5 +56,15 @@ struct MatmulParams {
 // Generic kernel: any size, stride and alignment (64 x 64 tiles).
 constexpr int kGenericRows = 64, kGenericCols = 64;
 const void* matmul_generic_kernel(int wd, bool gated);
+
+// Tiled kernels: rows of 16-byte blocks (hidden a multiple of eight, 16-byte
+// aligned rows of x and w) that 32-bit offsets reach.  mode: 0 dense, 1
+// grouped, 2 gated.
+struct TiledKernel {
+  const void* kernel;
+  int rows, cols, threads;  // of a tile, of a workgroup
+};
+TiledKernel matmul_tiled_large(int wd, int mode);
+TiledKernel matmul_tiled_medium(int wd, int mode);
 
 }  // namespace sgmv
