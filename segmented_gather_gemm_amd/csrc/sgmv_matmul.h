@@ -165,6 +165,17 @@ __device__ __forceinline__ void tile_adapters(const MatmulParams& p, int32_t row
   }
 }
 
+// Slice i's descriptor, read from the kernel's argument memory: a variable
+// index into the argument itself makes the compiler copy all of it to scratch
+// memory and read every field from there.  MatmulParams is the kernels' only
+// argument.
+__device__ __forceinline__ AdapterDesc adapter_desc(int i) {
+  typedef const __attribute__((address_space(4))) MatmulParams* Args;
+  const Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+  const auto& d = args->s[i];
+  return AdapterDesc{d.b, d.v, d.n, d.offset};
+}
+
 // Eight float32 values as two packed operands of the 16-bit weight dtype,
 // v = hi + lo to 16 (bfloat16) or 22 (float16) bits: one rounding to the
 // weights' dtype would leave the adapters' share of a float32 result with an

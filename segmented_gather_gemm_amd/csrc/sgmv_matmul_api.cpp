@@ -52,9 +52,12 @@ int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 // Whether the tiled kernels' 16-byte blocks and 32-bit offsets fit: hidden a
 // multiple of eight, aligned rows, and less than 2 GiB from the first to the
-// last row of a tile (gathered: of the inputs).
+// last row of a tile (gathered: of the inputs); adapters of ranks that are
+// multiples of eight, aligned and less than 2 GiB each.
 bool tiled_fits(const sgmv::MatmulParams& p) {
   const int64_t most = int64_t(1) << 31, rows = 256;
+  for (int i = 0; i < p.num_slices; ++i)
+    if (p.K % 8 != 0 || !aligned16(p.s[i].b) || p.s[i].n * p.K * 2 >= most) return false;
   return p.H % 8 == 0 && aligned16(p.x) && aligned16(p.w) && p.x_row_bytes % 16 == 0 &&
          p.w_row_bytes % 16 == 0 && p.w_mat_bytes % 16 == 0 && rows * p.w_row_bytes < most &&
          (p.rows ? p.X : rows) * p.x_row_bytes < most;
@@ -62,7 +65,7 @@ bool tiled_fits(const sgmv::MatmulParams& p) {
 
 sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan) {
   using namespace sgmv;
-  const int mode = gated ? 2 : p.grouped ? 1 : 0;
+  const int mode = gated ? 2 : p.grouped ? 1 : p.num_slices > 0 ? 3 : 0;
   if (tiled_fits(p)) {
     const TiledKernel k = matmul_tiled_large(wd, mode);
     *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0};
@@ -214,12 +217,8 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
   p.N = (int32_t)out.cols;
   p.out_dtype = out.dtype;
   p.add = add_inputs != 0;
-  Plan plan;
-  st = make_plan(p, weight.dtype, false, &plan);
-  if (st != SGMV_OK) return st;
+  sgmv_shrink_slice down[SGMV_MAX_SLICES];
   if (adapters) {
-    // First the projections onto the adapters' rank, kept in float32.
-    sgmv_shrink_slice down[SGMV_MAX_SLICES];
     p.start = b_seq_start_loc;
     p.lens = seq_lens;
     p.idx = lora_indices;
@@ -235,6 +234,12 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
       down[i].out = sgmv_matrix{v, SGMV_F32, x.rows, K, p.v_stride};
       p.s[i] = AdapterDesc{slices[i].lora_b.data, v, slices[i].lora_b.rows, slices[i].slice_offset};
     }
+  }
+  Plan plan;
+  st = make_plan(p, weight.dtype, false, &plan);
+  if (st != SGMV_OK) return st;
+  if (adapters) {
+    // First the projections onto the adapters' rank, kept in float32.
     st = sgmv_shrink_multi_slice(inputs, down, num_slices, b_seq_start_loc, seq_lens, lora_indices,
                                  batches, max_seq_len, scale, nullptr, 0, stream);
     if (st != SGMV_OK) return st;

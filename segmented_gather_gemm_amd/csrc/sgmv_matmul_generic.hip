@@ -61,8 +61,13 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
     for (int i = 0; i < adapters; ++i) {
       const int32_t a = uniform(list[i]);
       if (__ballot(my_a == a) == 0) continue;  // none of this wave's rows
+      // The sums go on from the accumulators and are kept in the lanes whose
+      // token has the adapter: its weights (a NaN, say) reach no other row.
+      f32x4 sum[kBlocks];
+#pragma unroll
+      for (int f = 0; f < kBlocks; ++f) sum[f] = acc[0][f];
       for (int s = 0; s < p.num_slices; ++s) {
-        const AdapterDesc& d = p.s[s];
+        const AdapterDesc d = adapter_desc(s);
         if (d.offset >= n0 + kGenericCols || d.offset + d.n <= n0) continue;
         const bool vb = ((reinterpret_cast<uintptr_t>(d.b) & 15) == 0) && p.K % 8 == 0;
         for (int k = 0; k < p.K; k += 32) {
@@ -70,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
           float v[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            v[j] = my_a == a && j < cnt ? d.v[(int64_t)row * p.v_stride + at + j] : 0.f;
+            v[j] = live && j < cnt ? d.v[(int64_t)row * p.v_stride + at + j] : 0.f;
           u32x4 hi, lo;
           split_operand<WD>(v, &hi, &lo);
 #pragma unroll
@@ -79,11 +84,15 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
             const bool in = n >= 0 && n < d.n;
             u32x4 bv;
             load_any8<WD>(d.b, ((int64_t)a * d.n + (in ? n : 0)) * p.K + at, in ? cnt : 0, vb, &bv);
-            acc[0][f] = mfma<WD>(bv, hi, acc[0][f]);
-            acc[0][f] = mfma<WD>(bv, lo, acc[0][f]);
+            sum[f] = mfma<WD>(bv, hi, sum[f]);
+            sum[f] = mfma<WD>(bv, lo, sum[f]);
           }
         }
       }
+#pragma unroll
+      for (int f = 0; f < kBlocks; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[0][f][j] = my_a == a ? sum[f][j] : acc[0][f][j];
     }
   }
 

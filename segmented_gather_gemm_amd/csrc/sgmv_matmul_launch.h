@@ -59,7 +59,7 @@ const void* matmul_generic_kernel(int wd, bool gated);
 
 // Tiled kernels: rows of 16-byte blocks (hidden a multiple of eight, 16-byte
 // aligned rows of x and w) that 32-bit offsets reach.  mode: 0 dense, 1
-// grouped, 2 gated.
+// grouped, 2 gated, 3 dense with adapters.
 struct TiledKernel {
   const void* kernel;
   int rows, cols, threads;  // of a tile, of a workgroup

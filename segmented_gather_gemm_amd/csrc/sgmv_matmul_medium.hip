@@ -7,16 +7,13 @@ namespace sgmv {
 
 TiledKernel matmul_tiled_medium(int wd, int mode) {
   using namespace dev;
-  using S = TileShape<2, 2, 2, 2>;
-  const void* k = nullptr;
-  if (wd == BF16)
-    k = mode == kDense     ? (const void*)matmul_tiled<BF16, kDense, S>
-        : mode == kGrouped ? (const void*)matmul_tiled<BF16, kGrouped, S>
-                           : (const void*)matmul_tiled<BF16, kGated, S>;
-  else if (wd == F16)
-    k = mode == kDense     ? (const void*)matmul_tiled<F16, kDense, S>
-        : mode == kGrouped ? (const void*)matmul_tiled<F16, kGrouped, S>
-                           : (const void*)matmul_tiled<F16, kGated, S>;
+  using S = TileShape<2, 2, 2, 2, 2>;
+  static const void* const kernels[2][4] = {
+      {(const void*)matmul_tiled<F16, kDense, S>, (const void*)matmul_tiled<F16, kGrouped, S>,
+       (const void*)matmul_tiled<F16, kGated, S>, (const void*)matmul_tiled<F16, kAdapted, S>},
+      {(const void*)matmul_tiled<BF16, kDense, S>, (const void*)matmul_tiled<BF16, kGrouped, S>,
+       (const void*)matmul_tiled<BF16, kGated, S>, (const void*)matmul_tiled<BF16, kAdapted, S>}};
+  const void* k = wd == F16 || wd == BF16 ? kernels[wd == BF16][mode] : nullptr;
   return TiledKernel{k, S::BM, mode == kGated ? S::HN : S::BN, S::kNT};
 }
 

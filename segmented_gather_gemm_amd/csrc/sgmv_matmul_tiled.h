@@ -15,16 +15,13 @@
 // slot.  Out-of-range rows and blocks (past the tile's rows, the matrix's
 // columns or the contraction) read zero through the buffer's bounds.
 //
-// A wave owns a quarter of its output in each pair of halves and goes through
-// them in four phases per step, (A0, Bx), (A0, By), (A1, By), (A1, Bx), with
-// the next step's x this step's y: a phase reads one new half into
-// registers, and the operands take 64 registers beside the accumulators'
-// 128.  Counting phases and halves in this order, phase q reads half q + 1
-// and refills the LDS of half q, which every wave has read, with half q + 8;
-// loads have six phases to arrive.  With eight waves the two waves of a SIMD
-// run half a phase apart: while one issues its matrix instructions, the other
-// reads its next operands and issues loads, and a barrier after each half
-// phase keeps them so.
+// A wave owns a quarter of the tile (a half of each half).  A step's matrix
+// instructions come in two parts of 32 along the contraction.  During part 1
+// all operands of the next step are read into registers (three sets of a
+// part's operands, rotating), so that its LDS is free half a step later:
+// during part 0 it is refilled with the step after next, whose loads then have
+// one and a half steps to arrive.  Barriers: before part 1 (the next step has
+// arrived, for every wave) and before part 0 (every wave has read it).
 #pragma once
 
 #include <type_traits>
@@ -34,15 +31,16 @@
 namespace sgmv {
 namespace dev {
 
-enum { kDense = 0, kGrouped = 1, kGated = 2 };
+enum { kDense = 0, kGrouped = 1, kGated = 2, kAdapted = 3 };  // kAdapted: dense with adapters
 
 typedef __attribute__((address_space(3))) void lds_void;
 
 // The shape of a tiled kernel: WM x WN waves, each FM x FN blocks of 16 x 16
 // per pair of halves.
-template <int WM_, int WN_, int FM_, int FN_>
+template <int WM_, int WN_, int FM_, int FN_, int OCC>
 struct TileShape {
   static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
+  static constexpr int kOccupancy = OCC;                       // waves per SIMD
   static constexpr int kWaves = WM * WN, kNT = 64 * kWaves;
   static constexpr int HM = WM * FM * 16, HN = WN * FN * 16;   // rows of a half
   static constexpr int BM = 2 * HM, BN = 2 * HN;
@@ -72,10 +70,75 @@ __device__ __forceinline__ void wait_lds_reads() {
   pin();
 }
 
+// make_rsrc of a wave-uniform range, said so (the compiler otherwise loops over
+// the lanes' descriptors at every load).
+__device__ __forceinline__ rsrc_t uniform_rsrc(const char* base, int64_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = (uint64_t)(uint32_t)uniform((int)(b >> 32)) << 32 | (uint32_t)uniform((int)b);
+  return make_rsrc(reinterpret_cast<const void*>(u), uniform(bytes <= 0 ? 0 : (int)bytes));
+}
+
+// c += a . b with c held in the accumulation registers.  Written out, because
+// the 256 x 256 tile's accumulators fill all 256 of them and the compiler
+// otherwise moves some of them at every step.  The compiler does not see a
+// matrix instruction here: what reads c next waits for mfma_done().
+template <int WD>
+__device__ __forceinline__ void mfma_into(f32x4& c, u32x4 a, u32x4 b) {
+  if constexpr (WD == BF16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// Two 16-bit values with those that are not finite replaced by zero.
+template <int WD>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t v) {
+  constexpr uint32_t kExp = WD == BF16 ? 0x7F80u : 0x7C00u;
+  const uint32_t lo = (v & kExp) == kExp ? 0u : v & 0xFFFFu;
+  const uint32_t hi = (v & kExp << 16) == kExp << 16 ? 0u : v & 0xFFFF0000u;
+  return hi | lo;
+}
+
+// What the weights of adapter a that are not finite add to out[row][n]: 0
+// nothing, 1 +inf, 2 -inf, 3 NaN.
+template <int WD>
+__device__ __forceinline__ uint8_t odd_products(const MatmulParams& p, int row, int a, int n) {
+  float sum = 0.f;
+  for (int s = 0; s < p.num_slices && a >= 0; ++s) {
+    const AdapterDesc d = adapter_desc(s);
+    if (n < d.offset || n >= d.offset + d.n) continue;
+    for (int k = 0; k < p.K; ++k) {
+      const float b = load_elem(d.b, ((int64_t)a * d.n + n - d.offset) * p.K + k, WD);
+      if (!__builtin_isfinite(b)) sum += d.v[(int64_t)row * p.v_stride + k] * b;
+    }
+  }
+  return sum == 0.f ? 0 : sum != sum ? 3 : sum > 0.f ? 1 : 2;
+}
+
+// Operands that other instructions wrote are there for mfma_into.
+__device__ __forceinline__ void mfma_ready() {
+  pin();
+  asm volatile("s_nop 7" ::: "memory");
+  pin();
+}
+
+// Block `quarter` + 4 s of row `row` of the block-th 16 rows of a half.
+__device__ __forceinline__ u32x4 operand_of(const uint16_t* src, int block, int s, int row,
+                                            int quarter) {
+  return *reinterpret_cast<const u32x4*>(src + (block * 16 + row) * 64 +
+                                         ((quarter + 4 * s) ^ (row & 7)) * 8);
+}
+
+// More wait states than a matrix instruction takes to write its result.
+__device__ __forceinline__ void mfma_done() {
+  pin();
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  pin();
+}
+
 template <int WD, int MODE, typename S>
-__global__ __launch_bounds__(S::kNT, 2) void matmul_tiled(MatmulParams p) {
+__global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulParams p) {
   constexpr int FM = S::FM, FN = S::FN, LL = S::kLoads, HM = S::HM, HN = S::HN;
-  constexpr bool kOffset = S::kWaves == 8;
   __shared__ uint16_t a00[HM * 64], a01[HM * 64], a10[HM * 64], a11[HM * 64];
   __shared__ uint16_t b00[HN * 64], b01[HN * 64], b10[HN * 64], b11[HN * 64];
   __shared__ int32_t sh[S::kWaves + 4];
@@ -92,10 +155,10 @@ __global__ __launch_bounds__(S::kNT, 2) void matmul_tiled(MatmulParams p) {
   // an offset per lane and load.  Weight rows: one resource per half.
   const int lr = lane >> 3;                  // row of a load's eight
   const int chunk = (lane & 7) ^ lr;         // 16-byte block this lane fetches
-  const bool gather = MODE != kDense && p.rows != nullptr;
+  const bool gather = (MODE == kGrouped || MODE == kGated) && p.rows != nullptr;
   const rsrc_t xr =
-      make_rsrc(static_cast<const char*>(p.x) + (gather ? 0 : loc.row) * p.x_row_bytes,
-                ((gather ? p.X : rows) - 1) * p.x_row_bytes + (int64_t)p.H * 2);
+      uniform_rsrc(static_cast<const char*>(p.x) + (gather ? 0 : loc.row) * p.x_row_bytes,
+                   ((gather ? p.X : rows) - 1) * p.x_row_bytes + (int64_t)p.H * 2);
   uint32_t xoff[2][LL], woff[LL];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -116,8 +179,9 @@ __global__ __launch_bounds__(S::kNT, 2) void matmul_tiled(MatmulParams p) {
     const int64_t first = MODE == kGated ? (int64_t)h * p.N + n0 : (int64_t)n0 + h * HN;
     const int64_t left = MODE == kGated ? p.N - n0 : (int64_t)p.N - n0 - h * HN;
     const int64_t nr = left < HN ? left : HN;
-    wr[h] = make_rsrc(static_cast<const char*>(p.w) + loc.e * p.w_mat_bytes + first * p.w_row_bytes,
-                      nr <= 0 ? 0 : (nr - 1) * p.w_row_bytes + (int64_t)p.H * 2);
+    wr[h] = uniform_rsrc(static_cast<const char*>(p.w) + loc.e * p.w_mat_bytes +
+                             first * p.w_row_bytes,
+                         nr <= 0 ? 0 : (nr - 1) * p.w_row_bytes + (int64_t)p.H * 2);
   }
   // LDS row f 16 + r of a block of 16 FN rows holds the weight row whose
   // products land, over the FN blocks, in one lane's consecutive columns:
@@ -130,166 +194,243 @@ __global__ __launch_bounds__(S::kNT, 2) void matmul_tiled(MatmulParams p) {
     woff[i] = (uint32_t)((int64_t)n * p.w_row_bytes) + chunk * 16;
   }
 
-  // Loads of half h of step t (nothing past the contraction).
-  auto load_a = [&](uint16_t* dst, int h, int t) __attribute__((always_inline)) {
-    const bool in = t * 64 + chunk * 8 < p.H;
-#pragma unroll
-    for (int i = 0; i < LL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xr, (lds_void*)(dst + (wave * LL + i) * 512), 16,
-          (int)(in ? xoff[h][i] + (uint32_t)t * 128u : kOut), 0, 0, 0);
+  const int steps = (p.H + 63) / 64;
+  // Load i of half h of step t, zeros past the contraction.
+  auto load_a = [&](uint16_t* dst, int h, int t, int i) __attribute__((always_inline)) {
+    const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(dst + (wave * LL + i) * 512), 16,
+                                             (int)(in ? xoff[h][i] : kOut), t * 128, 0, 0);
   };
-  auto load_b = [&](uint16_t* dst, int h, int t) __attribute__((always_inline)) {
-    const bool in = t * 64 + chunk * 8 < p.H;
-#pragma unroll
-    for (int i = 0; i < LL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wr[h], (lds_void*)(dst + (wave * LL + i) * 512), 16,
-          (int)(in ? woff[i] + (uint32_t)t * 128u : kOut), 0, 0, 0);
+  auto load_b = [&](uint16_t* dst, int h, int t, int i) __attribute__((always_inline)) {
+    const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[h], (lds_void*)(dst + (wave * LL + i) * 512), 16,
+                                             (int)(in ? woff[i] : kOut), t * 128, 0, 0);
   };
 
-  // Operands: row lane & 15 of a block of 16, block lane / 16 + 4 s of the
-  // row.  A wave whose rows of a half all lie past the tile skips them.
+  // Operands of part s: row lane & 15 of a block of 16, block lane / 16 + 4 s
+  // of the row.
   const int orow = lane & 15, oq = lane >> 4;
-  const bool live[2] = {wm * FM * 16 < rows, HM + wm * FM * 16 < rows};
-  u32x4 xa[FM][2], wb[2][FN][2];
-  f32x4 acc[2][2][FM][FN] = {};   // [A half][B half]
-  auto read_a = [&](const uint16_t* src, int h) __attribute__((always_inline)) {
-    if (!live[h]) return;
-#pragma unroll
-    for (int f = 0; f < FM; ++f)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        xa[f][s] = *reinterpret_cast<const u32x4*>(src + ((wm * FM + f) * 16 + orow) * 64 +
-                                                   ((oq + 4 * s) ^ (orow & 7)) * 8);
+  u32x4 xa[3][2 * FM], wb[3][2 * FN];   // three sets of a part's operands
+  f32x4 acc[2][2][FM][FN] = {};         // [A half][B half]
+  auto operand = [&](const uint16_t* src, int block, int s) __attribute__((always_inline)) {
+    return operand_of(src, block, s, orow, oq);
   };
-  auto read_b = [&](const uint16_t* src, int h) __attribute__((always_inline)) {
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        wb[h][f][s] = *reinterpret_cast<const u32x4*>(src + ((wn * FN + f) * 16 + orow) * 64 +
-                                                      ((oq + 4 * s) ^ (orow & 7)) * 8);
+  // Operand i of part s into set `to`: the 2 FN of B, then the 2 FM of A.
+  auto read_one = [&](const uint16_t* A0, const uint16_t* A1, const uint16_t* B0,
+                      const uint16_t* B1, int s, int to, int i) __attribute__((always_inline)) {
+    if (i < 2 * FN) wb[to][i] = operand(i < FN ? B0 : B1, wn * FN + i % FN, s);
+    else xa[to][i - 2 * FN] = operand(i - 2 * FN < FM ? A0 : A1, wm * FM + (i - 2 * FN) % FM, s);
   };
-  // The second half of a phase, between barriers.
-  auto products = [&](int ah, int bh) __attribute__((always_inline)) {
-    wait_loads<6 * LL>();
+  // Load i of a step: LL of each half.
+  auto load_one = [&](uint16_t* A0, uint16_t* A1, uint16_t* B0, uint16_t* B1, int t,
+                      int i) __attribute__((always_inline)) {
+    if (i < LL) load_b(B0, 0, t, i);
+    else if (i < 2 * LL) load_a(A0, 0, t, i - LL);
+    else if (i < 3 * LL) load_b(B1, 1, t, i - 2 * LL);
+    else load_a(A1, 1, t, i - 3 * LL);
+  };
+  constexpr int kReads = 2 * (FM + FN), kLoads = 4 * LL;
+  // Step t, whose operands are in sets 0 and 1 + t % 2, with its LDS
+  // (A0, A1, B0, B1) free and the next step's in (C0, C1, D0, D1).  BOTH:
+  // whether the second A half holds any row.
+  auto step = [&](uint16_t* A0, uint16_t* A1, uint16_t* B0, uint16_t* B1, uint16_t* C0,
+                  uint16_t* C1, uint16_t* D0, uint16_t* D1, int t, auto set,
+                  auto both) __attribute__((always_inline)) {
+    constexpr int kRows = decltype(both)::value ? 2 * FM : FM;
+    constexpr int kMfma = kRows * 2 * FN, kSet = decltype(set)::value;
+    auto rows_of = [&](int from, auto between) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < kMfma; ++k) {
+        const int m = k / (2 * FN), n = k % (2 * FN);
+        between(k);
+        mfma_into<WD>(acc[m / FM][n / FN][m % FM][n % FN], wb[from][n], xa[from][m]);
+      }
+    };
+    int loads = 0, reads = 0;
+    rows_of(0, [&](int k) __attribute__((always_inline)) {
+      if (loads * kMfma <= k * kLoads && loads < kLoads) {
+        pin();
+        load_one(A0, A1, B0, B1, t + 2, loads++);
+        pin();
+      }
+    });
+    wait_loads<kLoads>();
+    wg_barrier();
+    rows_of(kSet, [&](int k) __attribute__((always_inline)) {
+      // two reads at a time, all of them in three quarters of the part
+      if (reads * kMfma * 3 <= k * 8 * kReads && reads < 2 * kReads) {
+        pin();
+        read_one(C0, C1, D0, D1, reads / kReads, reads < kReads ? 0 : 3 - kSet, reads % kReads);
+        ++reads;
+        read_one(C0, C1, D0, D1, reads / kReads, reads < kReads ? 0 : 3 - kSet, reads % kReads);
+        ++reads;
+        pin();
+      }
+    });
     wait_lds_reads();
     wg_barrier();
-    if (live[ah]) {
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int m = 0; m < FM; ++m)
-#pragma unroll
-          for (int n = 0; n < FN; ++n)
-            acc[ah][bh][m][n] = mfma<WD>(wb[bh][n][s], xa[m][s], acc[ah][bh][m][n]);
-      __builtin_amdgcn_s_setprio(0);
-    }
-    wg_barrier();
-  };
-  // One step: its halves' LDS, the next step's first B half, x and y.
-  auto step = [&](uint16_t* A0, uint16_t* A1, uint16_t* Bx, uint16_t* By, uint16_t* next, int x,
-                  int t) __attribute__((always_inline)) {
-    const int y = 1 - x;
-    read_a(A0, 0);
-    load_b(Bx, x, t + 2);
-    products(0, x);
-    read_b(By, y);
-    load_a(A0, 0, t + 2);
-    products(0, y);
-    read_a(A1, 1);
-    load_b(By, y, t + 2);
-    products(1, y);
-    read_b(next, y);
-    load_a(A1, 1, t + 2);
-    products(1, x);
   };
 
-  const int steps = (p.H + 63) / 64;
-  load_b(b00, 0, 0);
-  load_a(a00, 0, 0);
-  load_b(b01, 1, 0);
-  load_a(a01, 1, 0);
-  load_b(b11, 1, 1);
-  load_a(a10, 0, 1);
-  load_b(b10, 0, 1);
-  load_a(a11, 1, 1);
-  wait_loads<6 * LL>();
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) load_one(a00, a01, b00, b01, 0, i);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) load_one(a10, a11, b10, b11, 1, i);
+  // Which adapters the tile's rows have, while the first loads are on their way.
+  __shared__ int32_t row_a[MODE == kAdapted ? S::BM : 4] __attribute__((aligned(16)));
+  __shared__ int32_t list[MODE == kAdapted ? S::BM : 1];
+  __shared__ int32_t count, odd_found;
+  if constexpr (MODE == kAdapted)
+    tile_adapters<S::kNT, S::BM>(p, loc.row, loc.end, row_a, list, &count);
+  wait_loads<kLoads>();
   wg_barrier();
-  read_b(b00, 0);
-  if (kOffset && wave >= S::kWaves / 2) wg_barrier();  // half a phase behind
-  int t = 0;
-  for (; t + 1 < steps; t += 2) {
-    step(a00, a01, b00, b01, b11, 0, t);
-    step(a10, a11, b11, b10, b00, 1, t + 1);
-  }
-  if (t < steps) step(a00, a01, b00, b01, b11, 0, t);
-  if (kOffset && wave < S::kWaves / 2) wg_barrier();
+#pragma unroll
+  for (int i = 0; i < 2 * kReads; ++i)
+    read_one(a00, a01, b00, b01, i / kReads, i / kReads, i % kReads);
+  wait_lds_reads();
+  wg_barrier();
+  auto contract = [&](auto both) __attribute__((always_inline)) {
+    // Two steps at a time, one of zeros after an odd number: a last single step
+    // makes the compiler move accumulators.
+    for (int t = 0; t < steps; t += 2) {
+      step(a00, a01, b00, b01, a10, a11, b10, b11, t, std::integral_constant<int, 1>{}, both);
+      step(a10, a11, b10, b11, a00, a01, b00, b01, t + 1, std::integral_constant<int, 2>{}, both);
+    }
+  };
+  if (rows > HM) contract(std::true_type{});
+  else contract(std::false_type{});
   wait_loads<0>();  // the loads past the last step write zeros: none may be on its way at the end
   wait_lds_reads();
 
-  // Columns of this lane: 4 FN consecutive ones in each B half.
-  const int col0 = n0 + wn * 16 * FN + oq * 4 * FN;
+  // The thread's number again, so that nothing derived from it below is kept
+  // in a register (or worse, in scratch memory, whose reloads would wait for
+  // the loads into LDS) during the contraction.
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int erow = tid & 15, eq = (tid >> 4) & 3;
 
-  if constexpr (MODE == kDense) {
-    if (p.num_slices > 0) {
-      __shared__ int32_t row_a[S::BM] __attribute__((aligned(16)));
-      __shared__ int32_t list[S::BM];
-      __shared__ int32_t count;
-      tile_adapters<S::kNT, S::BM>(p, loc.row, loc.end, row_a, list, &count);
-      const int32_t adapters = uniform(count);
-      for (int i = 0; i < adapters; ++i) {
-        const int32_t a = uniform(list[i]);
+  // Columns of this lane: 4 FN consecutive ones in each B half.
+  const int col0 = n0 + wn * 16 * FN + eq * 4 * FN;
+
+  // Adapters, as further steps of the contraction: for each slice and 64 of
+  // the rank, the tile's projected rows as two 16-bit parts (A0, A1 of the
+  // first buffer the high ones, of the second the low ones) and, one adapter
+  // after another, its lora_B rows (alternating between the B buffers, the
+  // next adapter's loads in flight during this one's products).  A row takes
+  // part with its own adapter and with zeros elsewhere; so that zero times
+  // what another request's weights hold is nothing, weights that are not
+  // finite are staged as zeros here and their products are added at the end,
+  // to the rows that have them.
+  [[maybe_unused]] bool odd_weights = false;
+  if constexpr (MODE == kAdapted) {
+    const int adapters = uniform(count);
+    constexpr int kA = S::BM * 8 / S::kNT, kB = S::BN * 8 / S::kNT;  // blocks per thread
+    if (tid == 0) odd_found = 0;
+    int mine[2 * FM];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          bool mine[FM];
-          uint64_t any = 0;
+    for (int m = 0; m < 2 * FM; ++m)
+      mine[m] = row_a[(m / FM) * HM + (wm * FM + m % FM) * 16 + erow];
+    for (int sl = 0; sl < (adapters > 0 ? p.num_slices : 0); ++sl) {
+      const AdapterDesc d = adapter_desc(sl);
+      if (d.offset >= n0 + S::BN || d.offset + d.n <= n0) continue;
+      const rsrc_t vr = uniform_rsrc(
+          reinterpret_cast<const char*>(d.v + (int64_t)loc.row * p.v_stride),
+          (int64_t)rows * p.v_stride * 4);
+      for (int k = 0; k < p.K; k += 64) {
+        u32x4 nb[kB];
+        auto load_lora_b = [&](int a) __attribute__((always_inline)) {
+          const rsrc_t br = uniform_rsrc(static_cast<const char*>(d.b) + a * d.n * p.K * 2,
+                                         d.n * p.K * 2);
 #pragma unroll
-          for (int m = 0; m < FM; ++m) {
-            mine[m] = row_a[h * HM + (wm * FM + m) * 16 + orow] == a;
-            any |= __ballot(mine[m]);
+          for (int j = 0; j < kB; ++j) {
+            const int u = tid + j * S::kNT, q = u >> 3, c = u & 7;
+            const int h = q / HN, in = q % HN, blk = in / (16 * FN);
+            const int f = in % (16 * FN) / 16, r = in % 16;
+            const int n = n0 + h * HN + blk * 16 * FN + (r >> 2) * 4 * FN + f * 4 + (r & 3) -
+                          (int)d.offset;
+            buf_load8<WD>(br,
+                          n >= 0 && k + c * 8 < p.K ? (uint32_t)(n * p.K + k + c * 8) * 2u : kOut,
+                          &nb[j]);
           }
-          if (any == 0) continue;
-          for (int sl = 0; sl < p.num_slices; ++sl) {
-            const AdapterDesc& d = p.s[sl];
-            if (d.offset >= n0 + S::BN || d.offset + d.n <= n0) continue;
-            const bool vb = ((reinterpret_cast<uintptr_t>(d.b) & 15) == 0) && p.K % 8 == 0;
-            for (int k = 0; k < p.K; k += 32) {
-              const int at = k + oq * 8, cnt = clamp8((int64_t)p.K - at);
-              u32x4 hi[FM], lo[FM];
+        };
+        auto store_lora_b = [&](uint16_t* B0, uint16_t* B1) __attribute__((always_inline)) {
+          bool odd = false;
 #pragma unroll
-              for (int m = 0; m < FM; ++m) {
-                const int64_t row = loc.row + h * HM + (wm * FM + m) * 16 + orow;
-                u32x4 raw[2];
-                load_any8<F32>(d.v, row * p.v_stride + at, mine[m] ? cnt : 0, true, raw);
-                float v[8];
-                out_values<F32>(raw, v);
-                split_operand<WD>(v, &hi[m], &lo[m]);
+          for (int j = 0; j < kB; ++j) {
+            const int u = tid + j * S::kNT, q = u >> 3, c = u & 7;
+            uint16_t* dst = q < HN ? B0 : B1;
+            u32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = finite_pair<WD>(nb[j][i]);
+            odd = odd || v[0] != nb[j][0] || v[1] != nb[j][1] || v[2] != nb[j][2] ||
+                  v[3] != nb[j][3];
+            *reinterpret_cast<u32x4*>(dst + (q % HN) * 64 + ((c ^ (q & 7)) * 8)) = v;
+          }
+          if (odd) odd_found = 1;
+        };
+        load_lora_b(uniform(list[0]));
+        __syncthreads();  // the LDS is free: last step's or last round's reads are over
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+          const int u = tid + j * S::kNT, r = u >> 3, c = u & 7;
+          u32x4 raw[2], hi, lo;
+          buf_load8<F32>(vr, k + c * 8 < p.K ? (uint32_t)(r * p.v_stride + k + c * 8) * 4u : kOut,
+                         raw);
+          float v[8];
+          out_values<F32>(raw, v);
+          split_operand<WD>(v, &hi, &lo);
+          const int at = (r % HM) * 64 + ((c ^ (r & 7)) * 8);
+          *reinterpret_cast<u32x4*>((r < HM ? a00 : a01) + at) = hi;
+          *reinterpret_cast<u32x4*>((r < HM ? a10 : a11) + at) = lo;
+        }
+        store_lora_b(b00, b01);
+        __syncthreads();
+        for (int i = 0; i < adapters; ++i) {
+          const int a = uniform(list[i]);
+          if (i + 1 < adapters) load_lora_b(uniform(list[i + 1]));
+          const uint16_t* B0 = i & 1 ? b10 : b00;
+          const uint16_t* B1 = i & 1 ? b11 : b01;
+          for (int s = 0; s < (p.K - k > 32 ? 2 : 1); ++s) {
+#pragma unroll
+            for (int n = 0; n < 2 * FN; ++n) wb[0][n] = operand_of(n < FN ? B0 : B1, wn * FN + n % FN, s, erow, eq);
+#pragma unroll
+            for (int m = 0; m < 2 * FM; ++m) {
+              if (__ballot(mine[m] == a) == 0) continue;  // none of these 16 rows
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                const uint16_t* A = m < FM ? (part ? a10 : a00) : (part ? a11 : a01);
+                u32x4 x = operand_of(A, wm * FM + m % FM, s, erow, eq);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = mine[m] == a ? x[j] : 0u;
+                mfma_ready();
+#pragma unroll
+                for (int n = 0; n < 2 * FN; ++n)
+                  mfma_into<WD>(acc[m / FM][n / FN][m % FM][n % FN], wb[0][n], x);
               }
-#pragma unroll
-              for (int bh = 0; bh < 2; ++bh)
-#pragma unroll
-                for (int f = 0; f < FN; ++f) {
-                  const int64_t n = (int64_t)n0 + bh * HN + wn * 16 * FN +
-                                    (orow >> 2) * 4 * FN + f * 4 + (orow & 3) - d.offset;
-                  const bool in = n >= 0 && n < d.n;
-                  u32x4 bv;
-                  load_any8<WD>(d.b, ((int64_t)a * d.n + (in ? n : 0)) * p.K + at, in ? cnt : 0,
-                                vb, &bv);
-#pragma unroll
-                  for (int m = 0; m < FM; ++m) {
-                    acc[h][bh][m][f] = mfma<WD>(bv, hi[m], acc[h][bh][m][f]);
-                    acc[h][bh][m][f] = mfma<WD>(bv, lo[m], acc[h][bh][m][f]);
-                  }
-                }
             }
           }
+          if (i + 1 < adapters) {
+            if (i & 1) store_lora_b(b00, b01);
+            else store_lora_b(b10, b11);
+          }
+          __syncthreads();
         }
       }
     }
+    odd_weights = adapters > 0 && uniform(odd_found) != 0;
+    if (odd_weights) {  // the A buffers, free now, take a code for every result
+#pragma unroll 1
+      for (int u = tid; u < S::BM * S::BN; u += S::kNT) {
+        const int r = u / S::BN, c = u % S::BN;
+        if (r < rows && n0 + c < p.N) {
+          uint16_t* part = r < HM ? (r < HM / 2 ? a00 : a01) : (r < HM + HM / 2 ? a10 : a11);
+          reinterpret_cast<uint8_t*>(part)[r % (HM / 2) * S::BN + c] =
+              odd_products<WD>(p, loc.row + r, row_a[r], n0 + c);
+        }
+      }
+      __syncthreads();
+    }
   }
+  mfma_done();
 
   auto finish = [&](auto od) __attribute__((always_inline)) {
     constexpr int OD = decltype(od)::value;
@@ -297,7 +438,7 @@ __global__ __launch_bounds__(S::kNT, 2) void matmul_tiled(MatmulParams p) {
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
-        const int r = h * HM + (wm * FM + m) * 16 + orow;
+        const int r = h * HM + (wm * FM + m) * 16 + erow;
         if (r >= rows) continue;
         char* out = static_cast<char*>(p.out) + (int64_t)(loc.row + r) * p.out_row_bytes;
 #pragma unroll
@@ -314,7 +455,20 @@ __global__ __launch_bounds__(S::kNT, 2) void matmul_tiled(MatmulParams p) {
               y[j] = MODE == kGated ? gate(acc[h][0][m][f][j & 3], acc[h][1][m][f][j & 3])
                                     : acc[h][bh][m][f][j & 3];
             }
-            if constexpr (MODE == kDense) {
+            if constexpr (MODE == kAdapted) {
+              if (odd_weights) {
+                const uint16_t* part = h == 0 ? (r < HM / 2 ? a00 : a01)
+                                              : (r < HM + HM / 2 ? a10 : a11);
+                const uint2 code = *reinterpret_cast<const uint2*>(
+                    reinterpret_cast<const uint8_t*>(part) + r % (HM / 2) * S::BN + col - n0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const uint32_t c = (j < 4 ? code.x : code.y) >> (8 * (j & 3)) & 3u;
+                  y[j] += c == 0 ? 0.f : c == 1 ? INFINITY : c == 2 ? -INFINITY : NAN;
+                }
+              }
+            }
+            if constexpr (MODE == kDense || MODE == kAdapted) {
               if (p.bias) {
                 u32x4 raw;
                 float b[8];

@@ -149,6 +149,27 @@ def test_lora_linear_nan_rows_stay_where_they_are(T):
     assert not torch.isfinite(o[bad].float()).any()
 
 
+@pytest.mark.parametrize("T", [12, 100, 260])
+@pytest.mark.parametrize("K", [8, 40])
+def test_lora_linear_nan_adapters_reach_their_own_rows_alone(T, K):
+    """An adapter whose weights hold NaN and infinities, between rows of other requests."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(2)
+    H, N, L = 136, 152, 3
+    x, w = normal(gen, T, H), normal(gen, N, H, sigma=H ** -0.5)
+    la, lb = normal(gen, L, K, H, sigma=H ** -0.5), normal(gen, L, N, K)
+    la[1, 0, 0], lb[1, :, K - 1] = float("inf"), float("nan")
+    idx = [(t * 7) % 4 - 1 for t in range(T)]
+    o = torch.zeros(T, N, dtype=BF16, device="cuda")
+    sg.sgmv_lora_linear(x, w, [(la, lb, 0)], o, i64(list(range(T))), i64([1] * T), i64(idx), T, 1)
+    keep = [t for t in range(T) if idx[t] != 1]
+    la, lb = la.clone(), lb.clone()
+    la[1], lb[1] = 0, 0
+    want, bound = U.lora_linear(x, w, None, [(la, lb, 0)], list(range(T)), [1] * T, idx, 1.0, o, False, BF16)
+    U.assert_within(o[keep], want[keep], bound[keep])
+    assert torch.isnan(o[[t for t in range(T) if idx[t] == 1]].float()).all()
+
+
 def grouped_case(lens, H, N, E=None, idx=None, rows=None, X=None, gated=False, dtype=BF16, out=None,
                  start=None, T=None, seed=0, pad_x=0, pad_out=0):
     import segmented_gather_gemm_amd as sg
