@@ -121,48 +121,52 @@ __device__ __forceinline__ TileLoc find_tile(const MatmulParams& p, int32_t tile
 // ---------------------------------------------------------------------------
 
 // Fill row_a[0 .. ROWS) with the adapter of rows row0 + i (-1: none) and
-// list[0 .. *count) with the distinct ones, in order of their first row (all
-// NT threads take part; NT >= ROWS; `count` is a word of LDS).  Segments are
-// disjoint, so every row is written by one thread at most.
+// list[0 .. *count) with the distinct ones, in any order (all NT threads take
+// part, NT >= ROWS; `segs` holds 3 ROWS words, `count` two; `mine` from
+// read_segment, which a caller can issue earlier).  Segments are disjoint, so
+// at most ROWS of them meet the tile; more (a broken precondition) are
+// dropped.
+struct Segment {
+  int64_t start, len, a;
+};
+__device__ __forceinline__ Segment read_segment(const MatmulParams& p, int32_t b) {
+  return b < p.batches ? Segment{p.start[b], p.lens[b], p.idx[b]} : Segment{0, 0, -1};
+}
+
 template <int NT, int ROWS>
-__device__ __forceinline__ void tile_adapters(const MatmulParams& p, int32_t row0, int32_t end,
-                                              int32_t* row_a, int32_t* list, int32_t* count) {
-  static_assert(NT >= ROWS && ROWS % 64 == 0, "one row per thread");
+__device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg, int32_t row0,
+                                              int32_t end, int32_t* row_a, int32_t* list,
+                                              int32_t* count, int32_t* segs) {
+  static_assert(NT >= ROWS, "one row per thread");
   const int tid = threadIdx.x;
-  if (tid < ROWS) row_a[tid] = -1;
-  if (tid == 0) *count = 0;
+  if (tid < 2) count[tid] = 0;
   __syncthreads();
   for (int32_t b = tid; b < p.batches; b += NT) {
-    const int64_t st = p.start[b], ln = p.lens[b], a = p.idx[b];
+    if (b >= NT) seg = read_segment(p, b);
+    const int64_t st = seg.start, ln = seg.len, a = seg.a;
     if (a < 0 || a >= p.L || ln <= 0 || st < 0 || st > p.T - ln) continue;
-    const int64_t lo = st > row0 ? st : row0, hi = st + ln < end ? st + ln : end;
-    for (int64_t r = lo; r < hi; ++r) row_a[r - row0] = (int32_t)a;
+    if (st >= end || st + ln <= row0) continue;
+    const int i = atomicAdd(&count[1], 1);
+    if (i >= ROWS) continue;
+    segs[i] = (int32_t)(st > row0 ? st - row0 : 0);
+    segs[ROWS + i] = (int32_t)((st + ln < end ? st + ln : end) - row0);
+    segs[2 * ROWS + i] = (int32_t)a;
   }
   __syncthreads();
-  // A row is listed when no earlier row has its adapter.
-  bool first = false;
-  int32_t mine = -1;
+  const int n = count[1] < ROWS ? count[1] : ROWS;
   if (tid < ROWS) {
-    mine = row_a[tid];
-    first = mine >= 0;
-    for (int i = 0; i < ROWS; i += 4) {
-      const int4 q = *reinterpret_cast<const int4*>(row_a + i);
-      first = first && !((q.x == mine && i < tid) || (q.y == mine && i + 1 < tid) ||
-                         (q.z == mine && i + 2 < tid) || (q.w == mine && i + 3 < tid));
+    int32_t mine = -1;
+    for (int i = 0; i < n; ++i)
+      mine = segs[i] <= tid && tid < segs[ROWS + i] ? segs[2 * ROWS + i] : mine;
+    row_a[tid] = mine;
+    if (tid < n) {  // an adapter is listed for its first segment here
+      const int32_t a = segs[2 * ROWS + tid];
+      bool first = true;
+      for (int i = 0; i < tid; ++i) first = first && segs[2 * ROWS + i] != a;
+      if (first) list[atomicAdd(&count[0], 1)] = a;
     }
   }
-  const uint64_t m = __ballot(first);
-  const int lane = tid & 63;
-  const int before = __builtin_popcountll(m & ((1ull << lane) - 1));
-#pragma unroll
-  for (int w = 0; w < ROWS / 64; ++w) {  // wave after wave, so that the order is the rows'
-    if (tid >> 6 == w) {
-      const int32_t at = *count;
-      if (first) list[at + before] = mine;
-      if (lane == 0) *count = at + __builtin_popcountll(m);
-    }
-    __syncthreads();
-  }
+  __syncthreads();
 }
 
 // Slice i's descriptor, read from the kernel's argument memory: a variable

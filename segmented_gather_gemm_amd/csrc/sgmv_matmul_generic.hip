@@ -15,9 +15,7 @@ namespace dev {
 template <int WD, bool GATED>
 __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   __shared__ int32_t sh[kWaves + 4];
-  __shared__ int32_t row_a[kGenericRows] __attribute__((aligned(16)));
-  __shared__ int32_t list[kGenericRows];
-  __shared__ int32_t count;
+  __shared__ int32_t row_a[kGenericRows], list[kGenericRows], segs[3 * kGenericRows], count[2];
   constexpr int kBlocks = kGenericCols / 16;
   const TileLoc loc = find_tile<kThreads>(p, kGenericRows, sh);
   if (loc.row < 0) return;
@@ -55,8 +53,8 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   }
 
   if (!GATED && p.num_slices > 0) {
-    tile_adapters<kThreads, kGenericRows>(p, loc.row, loc.end, row_a, list, &count);
-    const int32_t adapters = uniform(count);
+    tile_adapters<kThreads, kGenericRows>(p, read_segment(p, threadIdx.x), loc.row, loc.end, row_a, list, count, segs);
+    const int32_t adapters = uniform(count[0]);
     const int32_t my_a = row_a[wave * 16 + (lane & 15)];
     for (int i = 0; i < adapters; ++i) {
       const int32_t a = uniform(list[i]);

@@ -271,16 +271,20 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     wg_barrier();
   };
 
+  Segment seg{};
+  if constexpr (MODE == kAdapted) {
+    seg = read_segment(p, threadIdx.x);
+    pin();  // ahead of the loads into LDS: loads arrive in order
+  }
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) load_one(a00, a01, b00, b01, 0, i);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) load_one(a10, a11, b10, b11, 1, i);
   // Which adapters the tile's rows have, while the first loads are on their way.
-  __shared__ int32_t row_a[MODE == kAdapted ? S::BM : 4] __attribute__((aligned(16)));
-  __shared__ int32_t list[MODE == kAdapted ? S::BM : 1];
-  __shared__ int32_t count, odd_found;
+  __shared__ int32_t row_a[MODE == kAdapted ? S::BM : 1], list[MODE == kAdapted ? S::BM : 1];
+  __shared__ int32_t segs[MODE == kAdapted ? 3 * S::BM : 1], count[2], odd_found;
   if constexpr (MODE == kAdapted)
-    tile_adapters<S::kNT, S::BM>(p, loc.row, loc.end, row_a, list, &count);
+    tile_adapters<S::kNT, S::BM>(p, seg, loc.row, loc.end, row_a, list, count, segs);
   wait_loads<kLoads>();
   wg_barrier();
 #pragma unroll
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // to the rows that have them.
   [[maybe_unused]] bool odd_weights = false;
   if constexpr (MODE == kAdapted) {
-    const int adapters = uniform(count);
+    const int adapters = uniform(count[0]);
     constexpr int kA = S::BM * 8 / S::kNT, kB = S::BN * 8 / S::kNT;  // blocks per thread
     if (tid == 0) odd_found = 0;
     int mine[2 * FM];
