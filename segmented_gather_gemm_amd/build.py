@@ -33,7 +33,7 @@ SOURCES = [os.path.join(CSRC, f) for f in
             "sgmv_fused_api.cpp", "sgmv_fused_k1.hip", "sgmv_fused_k2.hip", "sgmv_fused_k4.hip",
             "sgmv_fused_k8.hip", "sgmv_valu.hip", "sgmv_matmul_api.cpp",
             "sgmv_matmul_generic.hip", "sgmv_matmul_large.hip", "sgmv_matmul_medium.hip",
-            "sgmv_route_api.cpp", "sgmv_route.hip")]
+            "sgmv_matmul_skinny.hip", "sgmv_route_api.cpp", "sgmv_route.hip")]
 
 STREAM_SOURCE = os.path.join(CSRC, "sgmv_stream.hip")
 STREAM_LIBRARY = os.path.join(HERE, "libsgmv_stream.so")

@@ -10,6 +10,17 @@
 namespace sgmv {
 namespace dev {
 
+// Kernel modes: dense, grouped, grouped with the SiLU gate, dense with adapters.
+enum { kDense = 0, kGrouped = 1, kGated = 2, kAdapted = 3 };
+
+// make_rsrc of a wave-uniform range, said so (the compiler otherwise loops over
+// the lanes' descriptors at every load).
+__device__ __forceinline__ rsrc_t uniform_rsrc(const char* base, int64_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = (uint64_t)(uint32_t)uniform((int)(b >> 32)) << 32 | (uint32_t)uniform((int)b);
+  return make_rsrc(reinterpret_cast<const void*>(u), uniform(bytes <= 0 ? 0 : (int)bytes));
+}
+
 // ---------------------------------------------------------------------------
 // Tiles.
 // ---------------------------------------------------------------------------

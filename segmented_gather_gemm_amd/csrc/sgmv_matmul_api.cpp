@@ -63,11 +63,24 @@ bool tiled_fits(const sgmv::MatmulParams& p) {
          (p.rows ? p.X : rows) * p.x_row_bytes < most;
 }
 
+// 256 x 256 tiles, one workgroup per compute unit, or 128 x 128 tiles, two:
+// whichever needs less time for the tiles that the fullest compute unit gets.
+sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode) {
+  const sgmv::TiledKernel l = sgmv::matmul_tiled_large(wd, mode);
+  const sgmv::TiledKernel m = sgmv::matmul_tiled_medium(wd, mode);
+  return (void)m, l;
+}
+
 sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan) {
   using namespace sgmv;
   const int mode = gated ? 2 : p.grouped ? 1 : p.num_slices > 0 ? 3 : 0;
   if (tiled_fits(p)) {
-    const TiledKernel k = matmul_tiled_large(wd, mode);
+    // Rows a weight matrix meets, on average over the segments.
+    const int64_t rows = p.grouped ? tiles(p.T, p.batches) : p.T;
+    const TiledKernel k = rows <= 16   ? matmul_skinny_16(wd, mode)
+                          : rows <= 32 ? matmul_skinny_32(wd, mode)
+                          : rows <= 64 ? matmul_skinny_64(wd, mode)
+                                       : pick_tiled(p, wd, mode);
     *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0};
   } else {
     *plan = Plan{matmul_generic_kernel(wd, gated), kGenericRows, kGenericCols, kThreads, 0, 0};

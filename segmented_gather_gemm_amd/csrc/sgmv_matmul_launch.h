@@ -66,5 +66,9 @@ struct TiledKernel {
 };
 TiledKernel matmul_tiled_large(int wd, int mode);
 TiledKernel matmul_tiled_medium(int wd, int mode);
+// Few rows: tiles of 16, 32 and 64 rows (the same requirements).
+TiledKernel matmul_skinny_16(int wd, int mode);
+TiledKernel matmul_skinny_32(int wd, int mode);
+TiledKernel matmul_skinny_64(int wd, int mode);
 
 }  // namespace sgmv

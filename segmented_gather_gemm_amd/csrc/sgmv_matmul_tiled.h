@@ -31,8 +31,6 @@
 namespace sgmv {
 namespace dev {
 
-enum { kDense = 0, kGrouped = 1, kGated = 2, kAdapted = 3 };  // kAdapted: dense with adapters
-
 typedef __attribute__((address_space(3))) void lds_void;
 
 // The shape of a tiled kernel: WM x WN waves, each FM x FN blocks of 16 x 16
@@ -68,14 +66,6 @@ __device__ __forceinline__ void wait_lds_reads() {
   pin();
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   pin();
-}
-
-// make_rsrc of a wave-uniform range, said so (the compiler otherwise loops over
-// the lanes' descriptors at every load).
-__device__ __forceinline__ rsrc_t uniform_rsrc(const char* base, int64_t bytes) {
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  const uint64_t u = (uint64_t)(uint32_t)uniform((int)(b >> 32)) << 32 | (uint32_t)uniform((int)b);
-  return make_rsrc(reinterpret_cast<const void*>(u), uniform(bytes <= 0 ? 0 : (int)bytes));
 }
 
 // c += a . b with c held in the accumulation registers.  Written out, because
