@@ -131,8 +131,9 @@ __device__ __forceinline__ TileLoc find_tile(const MatmulParams& p, int32_t tile
 // Adapters of a tile's rows.
 // ---------------------------------------------------------------------------
 
-// Fill row_a[0 .. ROWS) with the adapter of rows row0 + i (-1: none) and
-// list[0 .. *count) with the distinct ones, in any order (all NT threads take
+// Fill list[0 .. *count) with the distinct adapters of rows row0 .. end, in
+// any order, and row_pos[0 .. ROWS) with the place of row row0 + i's adapter in
+// it (-1: none) (all NT threads take
 // part, NT >= ROWS; `segs` holds 3 ROWS words, `count` two; `mine` from
 // read_segment, which a caller can issue earlier).  Segments are disjoint, so
 // at most ROWS of them meet the tile; more (a broken precondition) are
@@ -146,7 +147,7 @@ __device__ __forceinline__ Segment read_segment(const MatmulParams& p, int32_t b
 
 template <int NT, int ROWS>
 __device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg, int32_t row0,
-                                              int32_t end, int32_t* row_a, int32_t* list,
+                                              int32_t end, int32_t* row_pos, int32_t* list,
                                               int32_t* count, int32_t* segs) {
   static_assert(NT >= ROWS, "one row per thread");
   const int tid = threadIdx.x;
@@ -169,13 +170,20 @@ __device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg
     int32_t mine = -1;
     for (int i = 0; i < n; ++i)
       mine = segs[i] <= tid && tid < segs[ROWS + i] ? segs[2 * ROWS + i] : mine;
-    row_a[tid] = mine;
+    row_pos[tid] = mine;
     if (tid < n) {  // an adapter is listed for its first segment here
       const int32_t a = segs[2 * ROWS + tid];
       bool first = true;
       for (int i = 0; i < tid; ++i) first = first && segs[2 * ROWS + i] != a;
       if (first) list[atomicAdd(&count[0], 1)] = a;
     }
+  }
+  __syncthreads();
+  if (tid < ROWS) {
+    const int32_t mine = row_pos[tid], adapters = count[0];
+    int32_t pos = -1;
+    for (int i = 0; i < adapters; ++i) pos = mine >= 0 && list[i] == mine ? i : pos;
+    row_pos[tid] = pos;
   }
   __syncthreads();
 }

@@ -52,35 +52,63 @@ int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 // Whether the tiled kernels' 16-byte blocks and 32-bit offsets fit: hidden a
 // multiple of eight, aligned rows, and less than 2 GiB from the first to the
-// last row of a tile (gathered: of the inputs); adapters of ranks that are
+// last row of a tile (gathered inputs: of all of them); adapters of ranks that are
 // multiples of eight, aligned and less than 2 GiB each.
 bool tiled_fits(const sgmv::MatmulParams& p) {
   const int64_t most = int64_t(1) << 31, rows = 256;
   for (int i = 0; i < p.num_slices; ++i)
     if (p.K % 8 != 0 || !aligned16(p.s[i].b) || p.s[i].n * p.K * 2 >= most) return false;
   return p.H % 8 == 0 && aligned16(p.x) && aligned16(p.w) && p.x_row_bytes % 16 == 0 &&
-         p.w_row_bytes % 16 == 0 && p.w_mat_bytes % 16 == 0 && rows * p.w_row_bytes < most &&
+         p.w_row_bytes % 16 == 0 && p.w_mat_bytes % 16 == 0 && rows * p.w_row_bytes < most && rows * p.out_row_bytes < most &&
          (p.rows ? p.X : rows) * p.x_row_bytes < most;
 }
 
 // 256 x 256 tiles, one workgroup per compute unit, or 128 x 128 tiles, two:
-// whichever needs less time for the tiles that the fullest compute unit gets.
-sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode) {
+// whichever ends first, by the rounds of workgroups that each takes.  A round
+// of large tiles is taken as 100; of medium ones as 34 with one workgroup per
+// compute unit, 57 with two, and 75 past two rounds, where their twice as
+// many bytes per product bind (measured: dense, hidden 4096, 4096 columns,
+// 4096 rows 105.6 us on 256 large tiles and 120.1 us on 1024 medium ones, 2048
+// rows 84.5 and 60.6 us, 512 rows 79.8 and 30.2 us; grouped, 8 experts x 1024
+// rows, hidden 14336, 955 and 1197 us, 32 experts x 188 rows 133.3 and 119.8
+// us).  A segment fills half of its last tile on average.
+sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int cus) {
   const sgmv::TiledKernel l = sgmv::matmul_tiled_large(wd, mode);
   const sgmv::TiledKernel m = sgmv::matmul_tiled_medium(wd, mode);
-  return (void)m, l;
+  auto count = [&](const sgmv::TiledKernel& k) {
+    const int64_t rows = p.grouped ? (2 * p.T + p.batches * k.rows) / (2 * k.rows) : tiles(p.T, k.rows);
+    return rows * tiles(p.N, k.cols);
+  };
+  const int64_t nl = count(l), nm = count(m);
+  const int64_t tl = 100 * tiles(nl, cus);
+  const int64_t tm = nm <= cus ? 34 : nm <= 4 * cus ? 57 * tiles(nm, 2 * cus) : 75 * nm / (2 * cus);
+  return tl < tm ? l : m;
 }
 
 sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan) {
   using namespace sgmv;
   const int mode = gated ? 2 : p.grouped ? 1 : p.num_slices > 0 ? 3 : 0;
   if (tiled_fits(p)) {
-    // Rows a weight matrix meets, on average over the segments.
-    const int64_t rows = p.grouped ? tiles(p.T, p.batches) : p.T;
-    const TiledKernel k = rows <= 16   ? matmul_skinny_16(wd, mode)
-                          : rows <= 32 ? matmul_skinny_32(wd, mode)
-                          : rows <= 64 ? matmul_skinny_64(wd, mode)
-                                       : pick_tiled(p, wd, mode);
+    int cus = 0;
+    const hipError_t e = device_compute_units(&cus);
+    if (e != hipSuccess)
+      return fail(SGMV_ERR_HIP, "device query failed: %s", hipGetErrorString(e));
+    // The kernel for few rows where there would be few tiles: dense calls of
+    // up to 32 rows (64 with adapters, whose share its waves divide), and
+    // segments of up to 16 rows whose 128 x 128 tiles leave half of the compute
+    // units idle (hidden 4096, 4096 columns: 17 rows 11.4 us against 26.5 in
+    // medium tiles, 64 rows 25.4 and 27.1; with more columns the tiles win, 14336
+    // and 64 rows 49.0 and 28.5 us; 8 experts x 4 rows 20.9 and 18.2 us).
+    const TiledKernel m = matmul_tiled_medium(wd, mode);
+    const int64_t few = 32 * (p.num_slices > 0 ? 2 : 1);
+    const int64_t used = p.batches < p.T ? p.batches : p.T;
+    const bool skinny = p.grouped ? tiles(p.T, p.batches) <= 16 &&
+                                        2 * used * tiles(p.N, m.cols) <= cus
+                                  : p.T <= few;
+    const TiledKernel k = !skinny                   ? pick_tiled(p, wd, mode, cus)
+                          : p.grouped || p.T <= 16 ? matmul_skinny_16(wd, mode)
+                          : p.T <= 32              ? matmul_skinny_32(wd, mode)
+                                                   : matmul_skinny_64(wd, mode);
     *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0};
   } else {
     *plan = Plan{matmul_generic_kernel(wd, gated), kGenericRows, kGenericCols, kThreads, 0, 0};
@@ -97,8 +125,7 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
 sgmv_status launch(const Plan& plan, sgmv::MatmulParams& p, hipStream_t stream) {
   p.row_tiles = (int32_t)plan.row_tiles;
   p.col_tiles = (int32_t)plan.col_tiles;
-  p.vec_out = aligned16(p.out) && p.out_row_bytes % 16 == 0;
-  p.vec_bias = aligned16(p.bias);
+  p.vec_out = aligned16(p.out) && p.out_row_bytes % 16 == 0 && p.N % 8 == 0;
   void* args[] = {&p};
   const hipError_t e = hipLaunchKernel(plan.kernel, dim3((unsigned)(plan.row_tiles * plan.col_tiles)),
                                        dim3((unsigned)plan.threads), args, 0, stream);

@@ -15,7 +15,7 @@ namespace dev {
 template <int WD, bool GATED>
 __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   __shared__ int32_t sh[kWaves + 4];
-  __shared__ int32_t row_a[kGenericRows], list[kGenericRows], segs[3 * kGenericRows], count[2];
+  __shared__ int32_t row_pos[kGenericRows], list[kGenericRows], segs[3 * kGenericRows], count[2];
   constexpr int kBlocks = kGenericCols / 16;
   const TileLoc loc = find_tile<kThreads>(p, kGenericRows, sh);
   if (loc.row < 0) return;
@@ -53,12 +53,13 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   }
 
   if (!GATED && p.num_slices > 0) {
-    tile_adapters<kThreads, kGenericRows>(p, read_segment(p, threadIdx.x), loc.row, loc.end, row_a, list, count, segs);
+    tile_adapters<kThreads, kGenericRows>(p, read_segment(p, threadIdx.x), loc.row, loc.end,
+                                          row_pos, list, count, segs);
     const int32_t adapters = uniform(count[0]);
-    const int32_t my_a = row_a[wave * 16 + (lane & 15)];
+    const int32_t my_pos = row_pos[wave * 16 + (lane & 15)];
     for (int i = 0; i < adapters; ++i) {
       const int32_t a = uniform(list[i]);
-      if (__ballot(my_a == a) == 0) continue;  // none of this wave's rows
+      if (__ballot(my_pos == i) == 0) continue;  // none of this wave's rows
       // The sums go on from the accumulators and are kept in the lanes whose
       // token has the adapter: its weights (a NaN, say) reach no other row.
       f32x4 sum[kBlocks];
@@ -90,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
 #pragma unroll
       for (int f = 0; f < kBlocks; ++f)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[0][f][j] = my_a == a ? sum[f][j] : acc[0][f][j];
+        for (int j = 0; j < 4; ++j) acc[0][f][j] = my_pos == i ? sum[f][j] : acc[0][f][j];
     }
   }
 

@@ -43,8 +43,7 @@ struct MatmulParams {
   int32_t grouped;
   int32_t out_dtype;
   int32_t add;            // dense: accumulate onto out
-  int32_t vec_out;        // 16-byte accesses of eight columns of out are legal
-  int32_t vec_bias;       // ... of eight values of bias
+  int32_t vec_out;        // out's rows are 16-byte aligned and its columns a multiple of eight
   int32_t col_tiles;      // column tiles of the launch
   int32_t row_tiles;      // dense: row tiles; grouped: bound on them (the device counts)
   int32_t num_slices;     // adapters: slices, rank, v's row stride (floats)

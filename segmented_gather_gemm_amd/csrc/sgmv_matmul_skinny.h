@@ -65,28 +65,34 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
   // matrix instructions; lane quarter q holds blocks q and 4 + q of a row.
   const int steps = (p.H + 63) / 64;
   const int mine = (steps - wave + kW - 1) / kW;
-  u32x4 wv[2][G][kMats][NB][2], xv[2][G][MB][2];
+  u32x4 wv[G][kMats][NB][2], xv[G][MB][2];
   f32x4 acc[kMats][MB][NB] = {};
-  auto load = [&](int buf, int u) __attribute__((always_inline)) {
+  auto load = [&](int g, int u) __attribute__((always_inline)) {
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int s = 0; s < 2; ++s) {
+      const int k = (wave + u * kW) * 64 + s * 32 + lq * 8;
+      const bool in = u < mine && k < p.H;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int k = (wave + (u + g) * kW) * 64 + s * 32 + lq * 8;
-        const bool in = u + g < mine && k < p.H;
+      for (int t = 0; t < kMats; ++t)
 #pragma unroll
-        for (int t = 0; t < kMats; ++t)
+        for (int n = 0; n < NB; ++n)
+          buf_load8<WD>(wr[t], in ? woff[n] + k * 2u : kOut, &wv[g][t][n][s]);
 #pragma unroll
-          for (int n = 0; n < NB; ++n)
-            buf_load8<WD>(wr[t], in ? woff[n] + k * 2u : kOut, &wv[buf][g][t][n][s]);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-          buf_load8<WD>(xr, in ? xoff[m] + k * 2u : kOut, &xv[buf][g][m][s]);
-      }
+      for (int m = 0; m < MB; ++m) buf_load8<WD>(xr, in ? xoff[m] + k * 2u : kOut, &xv[g][m][s]);
+    }
   };
-  auto use = [&](int buf) __attribute__((always_inline)) {
+  Segment seg{};
+  if constexpr (MODE == kAdapted) seg = read_segment(p, threadIdx.x);
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+  for (int g = 0; g < G; ++g) load(g, g);
+  // Which adapters the tile's rows have, while the first loads are on their way.
+  __shared__ int32_t row_pos[MODE == kAdapted ? ROWS : 1], list[MODE == kAdapted ? ROWS : 1];
+  __shared__ int32_t segs[MODE == kAdapted ? 3 * ROWS : 1], count[2];
+  if constexpr (MODE == kAdapted)
+    tile_adapters<kNT, ROWS>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
+  for (int u = 0; u < mine; u += G) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {  // past the last step: zeros
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -95,69 +101,73 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
           for (int m = 0; m < MB; ++m)
 #pragma unroll
             for (int n = 0; n < NB; ++n)
-              acc[t][m][n] = mfma<WD>(wv[buf][g][t][n][s], xv[buf][g][m][s], acc[t][m][n]);
-  };
-  load(0, 0);
-  for (int u = 0; u < mine; u += 2 * G) {
-    load(1, u + G);
-    use(0);
-    load(0, u + 2 * G);
-    use(1);
+              acc[t][m][n] = mfma<WD>(wv[g][t][n][s], xv[g][m][s], acc[t][m][n]);
+      load(g, u + G + g);
+    }
   }
 
-  // Adapters, one after another dealt to the waves: each wave's products go
-  // to the lanes whose token has the adapter, so that what one request's
-  // weights hold never reaches another's rows.
+  // Adapters, dealt to the waves, kAtOnce of a wave's own at a time: each
+  // adapter's products go to the lanes whose token has it, so that what one
+  // request's weights hold never reaches another's rows.
   if constexpr (MODE == kAdapted) {
-    __shared__ int32_t row_a[ROWS], list[ROWS], segs[3 * ROWS], count[2];
-    tile_adapters<kNT, ROWS>(p, read_segment(p, threadIdx.x), loc.row, loc.end, row_a, list, count,
-                             segs);
+    constexpr int kAtOnce = 4;
     const int adapters = uniform(count[0]);
-    for (int i = wave; i < adapters; i += kW) {
-      const int a = uniform(list[i]);
-      f32x4 d[MB][NB] = {};
-      for (int sl = 0; sl < p.num_slices; ++sl) {
-        const AdapterDesc ad = adapter_desc(sl);
-        if (ad.offset >= n0 + 16 * NB || ad.offset + ad.n <= n0) continue;
-        const rsrc_t br = uniform_rsrc(static_cast<const char*>(ad.b) + a * ad.n * p.K * 2,
-                                       ad.n * p.K * 2);
-        const rsrc_t vr =
-            uniform_rsrc(reinterpret_cast<const char*>(ad.v + (int64_t)loc.row * p.v_stride),
-                         (int64_t)rows * p.v_stride * 4);
-        for (int k = 0; k < p.K; k += 32) {
-          const int at = k + lq * 8;
-          u32x4 bv[NB], hi[MB], lo[MB];
+    int pos[MB];
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            const int c = n0 + n * 16 + lr - (int)ad.offset;
-            buf_load8<WD>(br, c >= 0 && c < ad.n && at < p.K ? (uint32_t)(c * p.K + at) * 2u : kOut,
-                          &bv[n]);
-          }
+    for (int m = 0; m < MB; ++m) pos[m] = row_pos[m * 16 + lr];
+    for (int sl = 0; sl < (wave < adapters ? p.num_slices : 0); ++sl) {
+      const AdapterDesc ad = adapter_desc(sl);
+      if (ad.offset >= n0 + 16 * NB || ad.offset + ad.n <= n0) continue;
+      const rsrc_t vr =
+          uniform_rsrc(reinterpret_cast<const char*>(ad.v + (int64_t)loc.row * p.v_stride),
+                       (int64_t)rows * p.v_stride * 4);
+      for (int k = 0; k < p.K; k += 32) {
+        const int at = k + lq * 8;
+        u32x4 raw[MB][2], hi[MB], lo[MB];
 #pragma unroll
-          for (int m = 0; m < MB; ++m) {
-            u32x4 raw[2];
-            buf_load8<F32>(vr, at < p.K ? (uint32_t)((m * 16 + lr) * p.v_stride + at) * 4u : kOut,
-                           raw);
-            float v[8];
-            out_values<F32>(raw, v);
-            split_operand<WD>(v, &hi[m], &lo[m]);
-          }
+        for (int m = 0; m < MB; ++m)
+          buf_load8<F32>(vr, at < p.K ? (uint32_t)((m * 16 + lr) * p.v_stride + at) * 4u : kOut,
+                         raw[m]);
+        for (int i = wave; i < adapters; i += kW * kAtOnce) {
+          u32x4 bv[kAtOnce][NB];
 #pragma unroll
-          for (int m = 0; m < MB; ++m)
+          for (int j = 0; j < kAtOnce; ++j) {
+            const int a = uniform(list[i + j * kW < adapters ? i + j * kW : i]);
+            const rsrc_t br = uniform_rsrc(static_cast<const char*>(ad.b) + a * ad.n * p.K * 2,
+                                           ad.n * p.K * 2);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-              d[m][n] = mfma<WD>(bv[n], hi[m], d[m][n]);
-              d[m][n] = mfma<WD>(bv[n], lo[m], d[m][n]);
+              const int c = n0 + n * 16 + lr - (int)ad.offset;
+              buf_load8<WD>(br,
+                            c >= 0 && c < ad.n && at < p.K ? (uint32_t)(c * p.K + at) * 2u : kOut,
+                            &bv[j][n]);
             }
+          }
+          if (i == wave) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+              float v[8];
+              out_values<F32>(raw[m], v);
+              split_operand<WD>(v, &hi[m], &lo[m]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            if (i + j * kW >= adapters) continue;
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+              const bool own = pos[m] == i + j * kW;
+              if (__ballot(own) == 0) continue;
+#pragma unroll
+              for (int n = 0; n < NB; ++n) {
+                f32x4 d = mfma<WD>(bv[j][n], hi[m], f32x4{});
+                d = mfma<WD>(bv[j][n], lo[m], d);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[0][m][n][q] += own ? d[q] : 0.f;
+              }
+            }
+          }
         }
-      }
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const bool own = row_a[m * 16 + lr] == a;
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[0][m][n][j] += own ? d[m][n][j] : 0.f;
       }
     }
   }

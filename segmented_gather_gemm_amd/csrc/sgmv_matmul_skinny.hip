@@ -6,8 +6,8 @@
 namespace sgmv {
 
 TiledKernel matmul_skinny_16(int wd, int mode) {
-  return TiledKernel{wd == dev::BF16 ? dev::skinny_kernel<dev::BF16, 1, 1, 4>(mode)
-                                : dev::skinny_kernel<dev::F16, 1, 1, 4>(mode),
+  return TiledKernel{wd == dev::BF16 ? dev::skinny_kernel<dev::BF16, 1, 1, 2>(mode)
+                                : dev::skinny_kernel<dev::F16, 1, 1, 2>(mode),
                      16, 16, 64 * dev::kSkinnyWaves};
 }
 

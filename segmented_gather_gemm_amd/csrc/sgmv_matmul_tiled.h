@@ -271,10 +271,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) load_one(a10, a11, b10, b11, 1, i);
   // Which adapters the tile's rows have, while the first loads are on their way.
-  __shared__ int32_t row_a[MODE == kAdapted ? S::BM : 1], list[MODE == kAdapted ? S::BM : 1];
+  __shared__ int32_t row_pos[MODE == kAdapted ? S::BM : 1], list[MODE == kAdapted ? S::BM : 1];
   __shared__ int32_t segs[MODE == kAdapted ? 3 * S::BM : 1], count[2], odd_found;
   if constexpr (MODE == kAdapted)
-    tile_adapters<S::kNT, S::BM>(p, seg, loc.row, loc.end, row_a, list, count, segs);
+    tile_adapters<S::kNT, S::BM>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
   wait_loads<kLoads>();
   wg_barrier();
 #pragma unroll
@@ -309,7 +309,9 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // the rank, the tile's projected rows as two 16-bit parts (A0, A1 of the
   // first buffer the high ones, of the second the low ones) and, one adapter
   // after another, its lora_B rows (alternating between the B buffers, the
-  // next adapter's loads in flight during this one's products).  A row takes
+  // next ones' loads in flight during these products).  Ranks up to 8, 16 and
+  // 32 put 8, 4 and 2 adapters side by side into a step of 64, so that a tile
+  // of many single-token requests takes fewer of them.  A row takes
   // part with its own adapter and with zeros elsewhere; so that zero times
   // what another request's weights hold is nothing, weights that are not
   // finite are staged as zeros here and their products are added at the end,
@@ -319,10 +321,12 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     const int adapters = uniform(count[0]);
     constexpr int kA = S::BM * 8 / S::kNT, kB = S::BN * 8 / S::kNT;  // blocks per thread
     if (tid == 0) odd_found = 0;
+    // Width of an adapter in a step, log2 of 8 elements, and adapters a step.
+    const int wide = p.K <= 8 ? 0 : p.K <= 16 ? 1 : p.K <= 32 ? 2 : 3, side = 8 >> wide;
     int mine[2 * FM];
 #pragma unroll
     for (int m = 0; m < 2 * FM; ++m)
-      mine[m] = row_a[(m / FM) * HM + (wm * FM + m % FM) * 16 + erow];
+      mine[m] = row_pos[(m / FM) * HM + (wm * FM + m % FM) * 16 + erow];
     for (int sl = 0; sl < (adapters > 0 ? p.num_slices : 0); ++sl) {
       const AdapterDesc d = adapter_desc(sl);
       if (d.offset >= n0 + S::BN || d.offset + d.n <= n0) continue;
@@ -331,9 +335,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
           (int64_t)rows * p.v_stride * 4);
       for (int k = 0; k < p.K; k += 64) {
         u32x4 nb[kB];
-        auto load_lora_b = [&](int a) __attribute__((always_inline)) {
-          const rsrc_t br = uniform_rsrc(static_cast<const char*>(d.b) + a * d.n * p.K * 2,
-                                         d.n * p.K * 2);
+        auto load_lora_b = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
           for (int j = 0; j < kB; ++j) {
             const int u = tid + j * S::kNT, q = u >> 3, c = u & 7;
@@ -341,13 +343,16 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
             const int f = in % (16 * FN) / 16, r = in % 16;
             const int n = n0 + h * HN + blk * 16 * FN + (r >> 2) * 4 * FN + f * 4 + (r & 3) -
                           (int)d.offset;
-            buf_load8<WD>(br,
-                          n >= 0 && k + c * 8 < p.K ? (uint32_t)(n * p.K + k + c * 8) * 2u : kOut,
-                          &nb[j]);
+            const int pos = i + (c >> wide), at = k + ((c & ((1 << wide) - 1)) << 3);
+            const bool ok = n >= 0 && n < d.n && pos < adapters && at < p.K;
+            const int64_t e = ok ? ((int64_t)list[ok ? pos : 0] * d.n + n) * p.K + at : 0;
+            load_vec8<WD>(d.b, e, &nb[j]);  // the stack's first block where there is none
+#pragma unroll
+            for (int w = 0; w < 4; ++w) nb[j][w] = ok ? nb[j][w] : 0u;
           }
         };
         auto store_lora_b = [&](uint16_t* B0, uint16_t* B1) __attribute__((always_inline)) {
-          bool odd = false;
+          bool found = false;
 #pragma unroll
           for (int j = 0; j < kB; ++j) {
             const int u = tid + j * S::kNT, q = u >> 3, c = u & 7;
@@ -355,46 +360,49 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
             u32x4 v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = finite_pair<WD>(nb[j][i]);
-            odd = odd || v[0] != nb[j][0] || v[1] != nb[j][1] || v[2] != nb[j][2] ||
-                  v[3] != nb[j][3];
+            found = found || v[0] != nb[j][0] || v[1] != nb[j][1] || v[2] != nb[j][2] ||
+                    v[3] != nb[j][3];
             *reinterpret_cast<u32x4*>(dst + (q % HN) * 64 + ((c ^ (q & 7)) * 8)) = v;
           }
-          if (odd) odd_found = 1;
+          if (found) odd_found = 1;
         };
-        load_lora_b(uniform(list[0]));
+        load_lora_b(0);
         __syncthreads();  // the LDS is free: last step's or last round's reads are over
 #pragma unroll
         for (int j = 0; j < kA; ++j) {
           const int u = tid + j * S::kNT, r = u >> 3, c = u & 7;
           u32x4 raw[2], hi, lo;
-          buf_load8<F32>(vr, k + c * 8 < p.K ? (uint32_t)(r * p.v_stride + k + c * 8) * 4u : kOut,
-                         raw);
+          const int at = k + ((c & ((1 << wide) - 1)) << 3);
+          buf_load8<F32>(vr, at < p.K ? (uint32_t)(r * p.v_stride + at) * 4u : kOut, raw);
           float v[8];
           out_values<F32>(raw, v);
           split_operand<WD>(v, &hi, &lo);
-          const int at = (r % HM) * 64 + ((c ^ (r & 7)) * 8);
-          *reinterpret_cast<u32x4*>((r < HM ? a00 : a01) + at) = hi;
-          *reinterpret_cast<u32x4*>((r < HM ? a10 : a11) + at) = lo;
+          const int to = (r % HM) * 64 + ((c ^ (r & 7)) * 8);
+          *reinterpret_cast<u32x4*>((r < HM ? a00 : a01) + to) = hi;
+          *reinterpret_cast<u32x4*>((r < HM ? a10 : a11) + to) = lo;
         }
         store_lora_b(b00, b01);
         __syncthreads();
-        for (int i = 0; i < adapters; ++i) {
-          const int a = uniform(list[i]);
-          if (i + 1 < adapters) load_lora_b(uniform(list[i + 1]));
-          const uint16_t* B0 = i & 1 ? b10 : b00;
-          const uint16_t* B1 = i & 1 ? b11 : b01;
-          for (int s = 0; s < (p.K - k > 32 ? 2 : 1); ++s) {
+        bool odd = false;
+        for (int i = 0; i < adapters; i += side, odd = !odd) {
+          if (i + side < adapters) load_lora_b(i + side);
+          const uint16_t* B0 = odd ? b10 : b00;
+          const uint16_t* B1 = odd ? b11 : b01;
+          // the second 32 hold something: more of the rank, or more adapters
+          const int subs = (side == 1 ? p.K - k > 32 : i + side / 2 < adapters) ? 2 : 1;
+          for (int s = 0; s < subs; ++s) {
+            const int slot = i + ((eq + 4 * s) >> wide);  // the adapter of this lane's block
 #pragma unroll
             for (int n = 0; n < 2 * FN; ++n) wb[0][n] = operand_of(n < FN ? B0 : B1, wn * FN + n % FN, s, erow, eq);
 #pragma unroll
             for (int m = 0; m < 2 * FM; ++m) {
-              if (__ballot(mine[m] == a) == 0) continue;  // none of these 16 rows
+              if (__ballot(mine[m] == slot) == 0) continue;  // none of these 16 rows
 #pragma unroll
               for (int part = 0; part < 2; ++part) {
                 const uint16_t* A = m < FM ? (part ? a10 : a00) : (part ? a11 : a01);
                 u32x4 x = operand_of(A, wm * FM + m % FM, s, erow, eq);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = mine[m] == a ? x[j] : 0u;
+                for (int j = 0; j < 4; ++j) x[j] = mine[m] == slot ? x[j] : 0u;
                 mfma_ready();
 #pragma unroll
                 for (int n = 0; n < 2 * FN; ++n)
@@ -402,8 +410,8 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
               }
             }
           }
-          if (i + 1 < adapters) {
-            if (i & 1) store_lora_b(b00, b01);
+          if (i + side < adapters) {
+            if (odd) store_lora_b(b00, b01);
             else store_lora_b(b10, b11);
           }
           __syncthreads();
@@ -418,7 +426,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
         if (r < rows && n0 + c < p.N) {
           uint16_t* part = r < HM ? (r < HM / 2 ? a00 : a01) : (r < HM + HM / 2 ? a10 : a11);
           reinterpret_cast<uint8_t*>(part)[r % (HM / 2) * S::BN + c] =
-              odd_products<WD>(p, loc.row + r, row_a[r], n0 + c);
+              odd_products<WD>(p, loc.row + r, row_pos[r] < 0 ? -1 : list[row_pos[r]], n0 + c);
         }
       }
       __syncthreads();
@@ -426,67 +434,99 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   }
   mfma_done();
 
-  auto finish = [&](auto od) __attribute__((always_inline)) {
+  // Results: eight consecutive columns of a token per lane and access, with
+  // rows and columns past the tile's sent past the buffer's end instead of
+  // branched around.  VEC: 16-byte accesses, else element by element.
+  const rsrc_t orsrc = uniform_rsrc(static_cast<const char*>(p.out) + loc.row * p.out_row_bytes,
+                                    (int64_t)rows * p.out_row_bytes);
+  const rsrc_t brsrc = uniform_rsrc(static_cast<const char*>(p.bias), (int64_t)p.N * 2);
+  auto finish = [&](auto od, auto vec) __attribute__((always_inline)) {
     constexpr int OD = decltype(od)::value;
+    constexpr bool VEC = decltype(vec)::value;
+    constexpr uint32_t ob = OD == F32 ? 4 : 2;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int bh = 0; bh < (MODE == kGated ? 1 : 2); ++bh)
 #pragma unroll
-      for (int m = 0; m < FM; ++m) {
-        const int r = h * HM + (wm * FM + m) * 16 + erow;
-        if (r >= rows) continue;
-        char* out = static_cast<char*>(p.out) + (int64_t)(loc.row + r) * p.out_row_bytes;
+      for (int g = 0; g < FN / 2; ++g) {
+        const int col = col0 + bh * HN + g * 8;
+        float bias[8] = {};
+        if constexpr (MODE == kDense || MODE == kAdapted) {
+          if (p.bias) {
 #pragma unroll
-        for (int bh = 0; bh < (MODE == kGated ? 1 : 2); ++bh)
+            for (int j = 0; j < 8; ++j)
+              bias[j] = widen<WD>((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                  brsrc, (int)((uint32_t)(col + j) * 2u), 0, 0));
+          }
+        }
 #pragma unroll
-          for (int g = 0; g < FN / 2; ++g) {  // eight columns at a time
-            const int col = col0 + bh * HN + g * 8;
-            const int cnt = clamp8((int64_t)p.N - col);
-            if (cnt == 0) continue;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int m = 0; m < FM; ++m) {
+            const int r = h * HM + (wm * FM + m) * 16 + erow;
+            const uint32_t off = (uint32_t)(r * p.out_row_bytes) + (uint32_t)col * ob;
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int f = 2 * g + j / 4;
               y[j] = MODE == kGated ? gate(acc[h][0][m][f][j & 3], acc[h][1][m][f][j & 3])
-                                    : acc[h][bh][m][f][j & 3];
+                                    : acc[h][bh][m][f][j & 3] + bias[j];
             }
             if constexpr (MODE == kAdapted) {
               if (odd_weights) {
-                const uint16_t* part = h == 0 ? (r < HM / 2 ? a00 : a01)
+                const uint16_t* half = h == 0 ? (r < HM / 2 ? a00 : a01)
                                               : (r < HM + HM / 2 ? a10 : a11);
-                const uint2 code = *reinterpret_cast<const uint2*>(
-                    reinterpret_cast<const uint8_t*>(part) + r % (HM / 2) * S::BN + col - n0);
+                const uint2 codes = *reinterpret_cast<const uint2*>(
+                    reinterpret_cast<const uint8_t*>(half) + r % (HM / 2) * S::BN + col - n0);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                  const uint32_t c = (j < 4 ? code.x : code.y) >> (8 * (j & 3)) & 3u;
+                  const uint32_t c = (j < 4 ? codes.x : codes.y) >> (8 * (j & 3)) & 3u;
                   y[j] += c == 0 ? 0.f : c == 1 ? INFINITY : c == 2 ? -INFINITY : NAN;
                 }
               }
             }
-            if constexpr (MODE == kDense || MODE == kAdapted) {
-              if (p.bias) {
-                u32x4 raw;
-                float b[8];
-                load_any8<WD>(p.bias, col, cnt, p.vec_bias, &raw);
-                out_values<WD>(&raw, b);
+            u32x4 raw[raw_vecs<OD>()];
+            if constexpr (VEC) {
+              const uint32_t at = r < rows && col < p.N ? off : kOut;
+              if constexpr (MODE == kDense || MODE == kAdapted) {
+                if (p.add) {
+                  float o[8];
+                  buf_load8<OD>(orsrc, at, raw);
+                  out_values<OD>(raw, o);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] += b[j];
+                  for (int j = 0; j < 8; ++j) y[j] += o[j];
+                }
               }
-              if (p.add) {
-                u32x4 raw[raw_vecs<OD>()];
-                float o[8];
-                load_any8<OD>(out, col, cnt, p.vec_out, raw);
-                out_values<OD>(raw, o);
+              out_pack<OD>(y, raw);
+              buf_store8<OD>(orsrc, at, raw);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] += o[j];
+              for (int j = 0; j < 8; ++j) {
+                const int at = (int)(r < rows && col + j < p.N ? off + j * ob : kOut);
+                float o = 0.f;
+                if constexpr (OD == F32) {
+                  if (p.add)
+                    o = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(orsrc, at, 0, 0));
+                  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[j] + o), orsrc, at, 0, 0);
+                } else {
+                  if (p.add)
+                    o = widen<OD>((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(orsrc, at,
+                                                                                           0, 0));
+                  __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack2<OD>(y[j] + o, 0.f), orsrc,
+                                                        at, 0, 0);
+                }
               }
             }
-            store_any8<OD>(out, col, cnt, p.vec_out, y);
+            pin();  // one block's values at a time: the accumulators' copies must not pile up
           }
       }
   };
-  if (p.out_dtype == BF16) finish(std::integral_constant<int, BF16>{});
-  else if (p.out_dtype == F16) finish(std::integral_constant<int, F16>{});
-  else finish(std::integral_constant<int, F32>{});
+  auto finish_as = [&](auto vec) __attribute__((always_inline)) {
+    if (p.out_dtype == BF16) finish(std::integral_constant<int, BF16>{}, vec);
+    else if (p.out_dtype == F16) finish(std::integral_constant<int, F16>{}, vec);
+    else finish(std::integral_constant<int, F32>{}, vec);
+  };
+  if (p.vec_out) finish_as(std::true_type{});
+  else finish_as(std::false_type{});
 }
 
 }  // namespace dev
