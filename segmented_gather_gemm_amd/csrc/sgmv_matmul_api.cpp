@@ -107,8 +107,8 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
                                   : p.T <= few;
     const TiledKernel k = !skinny                   ? pick_tiled(p, wd, mode, cus)
                           : p.grouped || p.T <= 16 ? matmul_skinny_16(wd, mode)
-                          : p.T <= 32              ? matmul_skinny_32(wd, mode)
-                                                   : matmul_skinny_64(wd, mode);
+                          : p.T <= 32              ? matmul_skinny_32(wd, p.num_slices > 0)
+                                                   : matmul_skinny_64_adapted(wd);
     *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0};
   } else {
     *plan = Plan{matmul_generic_kernel(wd, gated), kGenericRows, kGenericCols, kThreads, 0, 0};

@@ -65,9 +65,10 @@ struct TiledKernel {
 };
 TiledKernel matmul_tiled_large(int wd, int mode);
 TiledKernel matmul_tiled_medium(int wd, int mode);
-// Few rows: tiles of 16, 32 and 64 rows (the same requirements).
+// Few rows (the same requirements): tiles of 16 rows, of 32 for dense calls
+// and of 64 for dense calls with adapters.
 TiledKernel matmul_skinny_16(int wd, int mode);
-TiledKernel matmul_skinny_32(int wd, int mode);
-TiledKernel matmul_skinny_64(int wd, int mode);
+TiledKernel matmul_skinny_32(int wd, bool adapted);
+TiledKernel matmul_skinny_64_adapted(int wd);
 
 }  // namespace sgmv

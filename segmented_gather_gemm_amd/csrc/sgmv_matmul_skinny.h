@@ -201,17 +201,5 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
   }
 }
 
-template <int WD, int MB, int NB, int G>
-const void* skinny_kernel(int mode) {
-  switch (mode) {
-    case kDense: return (const void*)matmul_skinny<WD, kDense, MB, NB, G>;
-    case kGrouped: return (const void*)matmul_skinny<WD, kGrouped, MB, NB, G>;
-    case kGated:
-      if constexpr (MB * NB < 8) return (const void*)matmul_skinny<WD, kGated, MB, NB, G>;
-      return nullptr;
-    default: return (const void*)matmul_skinny<WD, kAdapted, MB, NB, G>;
-  }
-}
-
 }  // namespace dev
 }  // namespace sgmv
