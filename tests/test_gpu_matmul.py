@@ -247,3 +247,85 @@ def test_grouped_many_segments():
     rng = np.random.default_rng(0)
     lens = rng.integers(0, 3, 900)
     grouped_case(lens.tolist(), 64, 32, E=5, idx=rng.integers(-1, 5, 900).tolist())
+
+
+# Enough tiles for the 256 x 256 kernel (its choice goes by the tile counts), with a last row tile
+# of less and of more than half, steps that end inside a block of 64, and columns that are no
+# multiple of eight.
+@pytest.mark.parametrize("T,H,N,dtype,out", [(4000, 136, 4000, BF16, BF16), (3900, 64, 4090, F16, F32),
+                                             (3850, 200, 4001, BF16, F16)])
+def test_lora_linear_large_tiles_without_adapters(T, H, N, dtype, out):
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T)
+    x, w = normal(gen, T, H, dtype=dtype), normal(gen, N, H, sigma=H ** -0.5, dtype=dtype)
+    b = normal(gen, N, dtype=dtype)
+    full, o = guarded(T, N, out, 6, gen)
+    o0 = o.clone()
+    none = i64([])
+    sg.sgmv_lora_linear(x, w, [], o, none, none, none, 0, 0, bias=b, add_inputs=True)
+    want, bound = U.lora_linear(x, w, b, [], [], [], [], 1.0, o0, True, out)
+    U.assert_within(o, want, bound)
+    assert bool((full[:, N:] == 7.0).all())
+
+
+@pytest.mark.parametrize("K", [8, 16, 32, 64, 104, 256])
+def test_lora_linear_large_tiles(K):
+    lens = [1, 700, 0, 259, 1024, 300, 17, 1, 1, 1300]
+    T = sum(lens) + 300
+    lora_case(T, 72, [2048, 1000, 950], K, 4, lens, [0, 1, 2, -1, 3, 2, 0, 1, 3, 2], dtype=F16 if K == 32 else BF16,
+              out=F32 if K == 64 else None, bias=True, seed=K)
+
+
+@pytest.mark.parametrize("K", [8, 16, 24, 40])
+def test_lora_linear_large_tiles_of_single_tokens(K):
+    T = 3900
+    rng = np.random.default_rng(K)
+    lora_case(T, 64, [4096], K, 40, [1] * T, rng.integers(-1, 40, T).tolist(), seed=K)
+
+
+@pytest.mark.parametrize("T,N", [(100, 152), (3900, 4096)])
+def test_lora_linear_odd_weights_in_tiles(T, N):
+    """Infinities and NaN among one adapter's weights: its rows get what IEEE arithmetic gives, other
+    rows nothing of it."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(4)
+    H, K, L = 72, 16, 3
+    x, w = normal(gen, T, H), normal(gen, N, H, sigma=H ** -0.5)
+    la, lb = normal(gen, L, K, H, sigma=H ** -0.5), normal(gen, L, N, K)
+    lb[1, 5, 3], lb[1, 9, 0], lb[1, 130, 2], lb[1, 130, 7] = float("inf"), float("nan"), float("-inf"), float("inf")
+    lens = [T // 3, T // 3, T - 2 * (T // 3)]
+    start, idx = [0, lens[0], 2 * lens[0]], [0, 1, 2]
+    o = torch.zeros(T, N, dtype=BF16, device="cuda")
+    sg.sgmv_lora_linear(x, w, [(la, lb, 0)], o, i64(start), i64(lens), i64(idx), 3, T)
+    y = x.double().cpu() @ w.double().cpu().t()
+    for st, n, a in zip(start, lens, idx):
+        v = x[st:st + n].double().cpu() @ la[a].double().cpu().t()
+        y[st:st + n] += (v[:, None, :] * lb[a].double().cpu()[None]).sum(dim=2) if T < 200 else v @ lb[a].double().cpu().t()
+    odd = ~torch.isfinite(y)
+    got = o.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(y)) and torch.equal(got[odd & ~torch.isnan(y)], y[odd & ~torch.isnan(y)])
+    clean = lb.clone()
+    clean[1] = torch.where(torch.isfinite(lb[1].float()), lb[1], torch.zeros_like(lb[1]))
+    want, bound = U.lora_linear(x, w, None, [(la, clean, 0)], start, lens, idx, 1.0, o, False, BF16)
+    U.assert_within(got[~odd], want[~odd], bound[~odd])
+
+
+@pytest.mark.parametrize("lens,H,N,gated,gather", [([1200, 0, 1100, 1400], 136, 4096, False, False),
+                                                   ([300, 1300, 1029, 1190], 72, 2040, True, True),
+                                                   ([3841], 64, 4001, False, True)])
+def test_grouped_large_tiles(lens, H, N, gated, gather):
+    rng = np.random.default_rng(H)
+    rows = rng.integers(-1, 500, sum(lens)).tolist() if gather else None
+    grouped_case(lens, H, N, rows=rows, X=499 if gather else None, gated=gated, dtype=F16 if gated else BF16,
+                 out=F32 if H == 64 else None, pad_out=5)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_grouped_few_rows_and_columns(gated):
+    """Too few tiles for the tiled kernels: the contraction is split over the waves."""
+    grouped_case([3, 0, 16, 1, 20], 1032, 136, gated=gated)
+
+
+@pytest.mark.parametrize("T", [70, 300])
+def test_lora_linear_columns_not_a_multiple_of_eight(T):
+    lora_case(T, 136, [131], 16, 2, [T], [1], bias=True, pad_out=3)
