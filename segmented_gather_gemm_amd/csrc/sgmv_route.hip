@@ -60,6 +60,38 @@ __device__ __forceinline__ float exp_below(float x, float m) {
   return x == m ? 1.f : __expf(x - m);
 }
 
+// Logits e0 .. e0 + V of a row; past E and NaN: -inf, never chosen.
+template <int V>
+__device__ __forceinline__ void load_logits(const char* row, int e0, int E, int dtype, bool vec,
+                                            float* x) {
+  if (V >= 4 && vec) {  // E is a multiple of V and rows are aligned for these loads
+    if (dtype == F32) {
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        const float4 q = e0 < E ? *reinterpret_cast<const float4*>(row + (e0 + v) * 4)
+                                : float4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        x[v] = q.x, x[v + 1] = q.y, x[v + 2] = q.z, x[v + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        uint2 q = e0 < E ? *reinterpret_cast<const uint2*>(row + (e0 + v) * 2) : uint2{0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t h = (i < 2 ? q.x : q.y) >> (16 * (i & 1)) & 0xFFFFu;
+          x[v + i] = e0 >= E ? -INFINITY : dtype == BF16 ? widen<BF16>(h) : widen<F16>(h);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      x[v] = e0 + v < E ? load_elem(row, e0 + v, dtype) : -INFINITY;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = x[v] == x[v] ? x[v] : -INFINITY;
+}
+
 // First slot of every expert from its total in `start` (in place), and the
 // number of all choices; all threads take part.
 __device__ __forceinline__ int32_t starts_of(int32_t* start, int E, int32_t* sh) {
@@ -99,13 +131,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_select(RouteParams p) {
       const bool live = t < r1;
       const char* row = static_cast<const char*>(p.logits) +
                         (int64_t)(live ? t : r1 - 1) * p.logits_row_bytes;
-      float x[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = sub + LPT * v;
-        x[v] = e < p.E ? load_elem(row, e, p.dtype) : -INFINITY;
-        x[v] = x[v] == x[v] ? x[v] : -INFINITY;  // NaN: never chosen
-      }
+      float x[V];  // experts sub V ..: consecutive, so that a whole lane's take one or two loads
+      load_logits<V>(row, sub * V, p.E, p.dtype, p.vec, x);
       float top = 0.f, over = 0.f;
       float w0 = 0.f, w1 = 0.f;      // this lane's choices: j = sub and j = sub + LPT
       int32_t e0 = -1, e1 = -1;
@@ -116,7 +143,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_select(RouteParams p) {
         for (int v = 0; v < V; ++v) {
           const bool take = x[v] > best;
           best = take ? x[v] : best;
-          e = take ? sub + LPT * v : e;
+          e = take ? sub * V + v : e;
         }
         reduce_best<LPT>(&best, &e);
         const bool none = best == -INFINITY;
@@ -139,7 +166,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_select(RouteParams p) {
           e1 = none ? -1 : e;
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) x[v] = e == sub + LPT * v ? -INFINITY : x[v];
+        for (int v = 0; v < V; ++v) x[v] = e == sub * V + v ? -INFINITY : x[v];
       }
       if (live) {
 #pragma unroll
@@ -214,13 +241,32 @@ __global__ __launch_bounds__(kRouteThreads) void route_place(RouteParams p) {
   // whole numbers, so the order of the adds does not matter.
   const int groups = p.E < kRouteThreads ? kRouteThreads / p.E : 1;
   const int g = p.E < kRouteThreads ? tid / p.E : 0;
+  // The first choices of this workgroup (often all of them) are read meanwhile.
+  const int32_t i0 = (int32_t)blockIdx.x * p.block_tokens * p.k;
+  const int32_t end = p.T * p.k;
+  const int32_t i1 = end - i0 > p.block_tokens * p.k ? i0 + p.block_tokens * p.k : end;
+  int32_t e1 = -1, s1 = 0;
+  if (i0 + tid < i1) {
+    e1 = (int32_t)p.experts[i0 + tid];
+    s1 = (int32_t)p.slots[i0 + tid];
+  }
   if (g < groups) {
     for (int e = p.E < kRouteThreads ? tid % p.E : tid; e < p.E; e += kRouteThreads) {
       int32_t all = 0, mine = 0;
-      for (int b = g; b < p.blocks; b += groups) {
-        const int32_t c = p.counts[(int64_t)b * p.E + e];
-        all += c;
-        mine += b < (int)blockIdx.x ? c : 0;
+      constexpr int kAtOnce = 8;  // loads in flight
+      for (int b = g; b < p.blocks; b += groups * kAtOnce) {
+        int32_t c[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int at = b + j * groups;
+          c[j] = p.counts[(int64_t)(at < p.blocks ? at : b) * p.E + e];
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int at = b + j * groups;
+          all += at < p.blocks ? c[j] : 0;
+          mine += at < (int)blockIdx.x ? c[j] : 0;
+        }
       }
       if (all) atomicAdd(&total[e], all);
       if (mine) atomicAdd(&before[e], mine);
@@ -232,14 +278,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_place(RouteParams p) {
   const int32_t used = starts_of(total, p.E, sh);
   if (blockIdx.x == 0)
     for (int e = tid; e < p.E; e += kRouteThreads) p.start[e] = total[e];
-  const int64_t i0 = (int64_t)blockIdx.x * p.block_tokens * p.k;
-  const int64_t end = (int64_t)p.T * p.k;
-  const int64_t i1 = i0 + (int64_t)p.block_tokens * p.k < end ? i0 + (int64_t)p.block_tokens * p.k
-                                                              : end;
-  for (int64_t i = i0 + tid; i < i1; i += kRouteThreads) {
-    const int32_t e = (int32_t)p.experts[i];
+  for (int32_t i = i0 + tid; i < i1; i += kRouteThreads) {
+    const bool first = i == i0 + tid;
+    const int32_t e = first ? e1 : (int32_t)p.experts[i];
     if (e < 0) continue;
-    const int64_t slot = (int64_t)total[e] + before[e] + p.slots[i];
+    const int32_t slot = total[e] + before[e] + (first ? s1 : (int32_t)p.slots[i]);
     p.slots[i] = slot;
     p.rows[slot] = i / p.k;
   }
@@ -292,6 +335,13 @@ const void* route_select_kernel(int experts) {
   if (experts <= 256) return (const void*)route_select<16, 16>;
   if (experts <= 512) return (const void*)route_select<64, 8>;
   return (const void*)route_select<64, 16>;
+}
+
+int route_lane_experts(int experts) {
+  const int lanes = experts <= 256 ? 16 : 64;
+  int v = 1;
+  while (lanes * v < experts) v <<= 1;
+  return v;
 }
 
 const void* route_place_kernel() { return (const void*)dev::route_place; }

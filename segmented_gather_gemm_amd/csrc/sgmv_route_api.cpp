@@ -98,6 +98,8 @@ sgmv_status sgmv_route(sgmv_matrix logits, int64_t top_k, int renormalize, float
   p.k = (int32_t)top_k;
   p.dtype = logits.dtype;
   p.renormalize = renormalize != 0;
+  p.vec = p.E % route_lane_experts(p.E) == 0 && aligned16(logits.data) &&
+          p.logits_row_bytes % 16 == 0;
   int64_t blocks, per, round;
   route_split(logits.rows, top_k, &blocks, &per, &round);
   if (blocks < 1) blocks = 1;  // no token: the empty segments are still written

@@ -27,6 +27,7 @@ struct RouteParams {
   int32_t T, E, k;
   int32_t dtype;
   int32_t renormalize;
+  int32_t vec;            // rows aligned for loads of a lane's experts, which divide E
   int32_t blocks;
   int32_t block_tokens;   // tokens of a workgroup
   int32_t round_tokens;   // tokens of a round: round_tokens * k <= kRouteEntries
@@ -35,6 +36,7 @@ struct RouteParams {
 // Selection kernel for E experts, and the kernel that places the choices
 // (calls of more than one workgroup).
 const void* route_select_kernel(int experts);
+int route_lane_experts(int experts);  // consecutive experts a lane of it holds
 const void* route_place_kernel();
 
 struct CombineParams {
