@@ -11,6 +11,12 @@
 // route_place: every workgroup adds up the counts of the ones before it and
 // writes each choice's slot and each slot's token.
 // Calls of one workgroup place their choices in route_select itself.
+//
+// Bound by the latency of its passes over registers and LDS, not by memory:
+// 16384 tokens, 128 experts, 8 choices 13 us + 7 us for 7.9 MB; 32 tokens of 64
+// experts 5.6 us in one launch.  16 lanes a token keep the butterfly within the
+// rotations of a row; up to 256 workgroups keep the counts that every one of
+// them reads to 256 rows (reading them one at a time cost 19 us instead of 7).
 #include "sgmv_matmul.h"
 #include "sgmv_route_launch.h"
 
@@ -291,7 +297,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_place(RouteParams p) {
 
 // out[t] = (add ? out[t] : 0) + sum_j weights[t][j] rows[slots[t][j]]: eight
 // columns a thread, the k rows in order, sums in float32, one rounding.
-// Bound by memory: every row is read once.
+// Bound by memory: every row is read once (16384 tokens, 8 rows of 2048 each,
+// bfloat16: 123 us, 4.8 TB/s; a large copy here runs at 5.1).
 template <int D>
 __global__ __launch_bounds__(kCombineThreads) void combine(CombineParams p) {
   const int64_t blocks8 = (p.H + 7) / 8;
