@@ -18,9 +18,11 @@
 // A wave owns a quarter of the tile (a half of each half).  A step's matrix
 // instructions come in two parts of 32 along the contraction.  During part 1
 // all operands of the next step are read into registers (three sets of a
-// part's operands, rotating), so that its LDS is free half a step later:
-// during part 0 it is refilled with the step after next, whose loads then have
-// one and a half steps to arrive.  Barriers: before part 1 (the next step has
+// part's operands, rotating), so that its LDS is free half a step later and is
+// refilled with the step after next during part 0 (five eighths of the loads)
+// and part 1; the loads have one to one and a half steps to arrive.  Evenly
+// spread they cost least: all of them in part 0 is 1-4% slower, in the first
+// half of part 0 6-8%.  Barriers: before part 1 (the next step has
 // arrived, for every wave) and before part 0 (every wave has read it).
 //
 // What bounds it: with 256 x 256 tiles the matrix instructions (busy 77% of the
@@ -229,6 +231,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     else load_a(A1, 1, t, i - 3 * LL);
   };
   constexpr int kReads = 2 * (FM + FN), kLoads = 4 * LL;
+  constexpr int kEarly = kLoads * 5 / 8;  // loads of a step that part 0 issues
   // Step t, whose operands are in sets 0 and 1 + t % 2, with its LDS
   // (A0, A1, B0, B1) free and the next step's in (C0, C1, D0, D1).  BOTH:
   // whether the second A half holds any row.
@@ -247,15 +250,20 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     };
     int loads = 0, reads = 0;
     rows_of(0, [&](int k) __attribute__((always_inline)) {
-      if (loads * kMfma <= k * kLoads && loads < kLoads) {
+      if (loads * kMfma <= k * kEarly && loads < kEarly) {
         pin();
         load_one(A0, A1, B0, B1, t + 2, loads++);
         pin();
       }
     });
-    wait_loads<kLoads>();
+    wait_loads<kEarly>();
     wg_barrier();
     rows_of(kSet, [&](int k) __attribute__((always_inline)) {
+      if ((loads - kEarly) * kMfma <= k * (kLoads - kEarly) && loads < kLoads) {
+        pin();
+        load_one(A0, A1, B0, B1, t + 2, loads++);
+        pin();
+      }
       // two reads at a time, all of them in three quarters of the part
       if (reads * kMfma * 3 <= k * 8 * kReads && reads < 2 * kReads) {
         pin();
