@@ -19,10 +19,9 @@
 // instructions come in two parts of 32 along the contraction.  During part 1
 // all operands of the next step are read into registers (three sets of a
 // part's operands, rotating), so that its LDS is free half a step later and is
-// refilled with the step after next during part 0 (five eighths of the loads)
-// and part 1; the loads have one to one and a half steps to arrive.  Evenly
-// spread they cost least: all of them in part 0 is 1-4% slower, in the first
-// half of part 0 6-8%.  Barriers: before part 1 (the next step has
+// refilled with the step after next, most of it during part 0; the loads have
+// one to one and a half steps to arrive.  Evenly spread they cost least: all
+// of them in the first half of part 0 is 6-8% slower.  Barriers: before part 1 (the next step has
 // arrived, for every wave) and before part 0 (every wave has read it).
 //
 // What bounds it: with 256 x 256 tiles the matrix instructions (busy 77% of the
@@ -231,7 +230,13 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     else load_a(A1, 1, t, i - 3 * LL);
   };
   constexpr int kReads = 2 * (FM + FN), kLoads = 4 * LL;
-  constexpr int kEarly = kLoads * 5 / 8;  // loads of a step that part 0 issues
+  // Loads of a step that part 0 issues.  Dense 16384 x 28672 x 4096: 10 of 16
+  // 2670 us, 12 2690, all 2755; with adapters beside it 3210, 3220 and 3062 us
+  // (the same instructions in the loop; why is open); small tiles over 64
+  // experts 5 of 8 187 us, 6 180, all 182.
+  constexpr int kEarly = MODE == kAdapted       ? kLoads
+                         : S::kOccupancy == 1 ? kLoads * 5 / 8
+                                              : kLoads * 3 / 4;
   // Step t, whose operands are in sets 0 and 1 + t % 2, with its LDS
   // (A0, A1, B0, B1) free and the next step's in (C0, C1, D0, D1).  BOTH:
   // whether the second A half holds any row.
