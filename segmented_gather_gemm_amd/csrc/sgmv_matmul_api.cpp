@@ -264,23 +264,24 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
     p.idx = lora_indices;
     p.batches = (int32_t)batches;
     p.L = (int32_t)L;
-    p.num_slices = num_slices;
     p.K = (int32_t)K;
     p.v_stride = (int32_t)projected_stride(K);
     for (int i = 0; i < num_slices; ++i) {
+      if (slices[i].lora_b.rows == 0) continue;  // no column (and maybe no data)
+      const int j = p.num_slices++;
       float* v = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                          i * projected_bytes(x.rows, K));
-      down[i].lora_a = slices[i].lora_a;
-      down[i].out = sgmv_matrix{v, SGMV_F32, x.rows, K, p.v_stride};
-      p.s[i] = AdapterDesc{slices[i].lora_b.data, v, slices[i].lora_b.rows, slices[i].slice_offset};
+                                          j * projected_bytes(x.rows, K));
+      down[j].lora_a = slices[i].lora_a;
+      down[j].out = sgmv_matrix{v, SGMV_F32, x.rows, K, p.v_stride};
+      p.s[j] = AdapterDesc{slices[i].lora_b.data, v, slices[i].lora_b.rows, slices[i].slice_offset};
     }
   }
   Plan plan;
   st = make_plan(p, weight.dtype, false, &plan);
   if (st != SGMV_OK) return st;
-  if (adapters) {
+  if (p.num_slices > 0) {
     // First the projections onto the adapters' rank, kept in float32.
-    st = sgmv_shrink_multi_slice(inputs, down, num_slices, b_seq_start_loc, seq_lens, lora_indices,
+    st = sgmv_shrink_multi_slice(inputs, down, p.num_slices, b_seq_start_loc, seq_lens, lora_indices,
                                  batches, max_seq_len, scale, nullptr, 0, stream);
     if (st != SGMV_OK) return st;
   }

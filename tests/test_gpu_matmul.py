@@ -329,3 +329,19 @@ def test_grouped_few_rows_and_columns(gated):
 @pytest.mark.parametrize("T", [70, 300])
 def test_lora_linear_columns_not_a_multiple_of_eight(T):
     lora_case(T, 136, [131], 16, 2, [T], [1], bias=True, pad_out=3)
+
+
+@pytest.mark.parametrize("T", [9, 150, 3900])
+def test_lora_linear_slices_without_columns(T):
+    """A slice of width 0 (whose weights have no memory) among others, and alone."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T)
+    H, N, K, L = 64, 4096 if T > 1000 else 160, 16, 2
+    x, w = normal(gen, T, H), normal(gen, N, H, sigma=1 / 8)
+    la, lb = normal(gen, L, K, H, sigma=1 / 8), normal(gen, L, N, K)
+    none = (la, torch.empty(L, 0, K, dtype=BF16, device="cuda"), 50)
+    for slices in ([none, (la, lb, 0)], [none]):
+        o = torch.zeros(T, N, dtype=BF16, device="cuda")
+        sg.sgmv_lora_linear(x, w, slices, o, i64([0]), i64([T]), i64([1]), 1, T)
+        want, bound = U.lora_linear(x, w, None, [s for s in slices if s[1].shape[1]], [0], [T], [1], 1.0, o, False, BF16)
+        U.assert_within(o, want, bound)
