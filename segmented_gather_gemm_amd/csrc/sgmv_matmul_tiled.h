@@ -195,16 +195,20 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   }
 
   const int steps = (p.H + 63) / 64;
-  // Load i of half h of step t, zeros past the contraction.
+  // Load i of half h of step t, zeros past the contraction.  The step is part
+  // of the lane's offset, which alone is certain to be held against the
+  // resource's end (a half of the weights may have no row at all).
   auto load_a = [&](uint16_t* dst, int h, int t, int i) __attribute__((always_inline)) {
     const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(dst + (wave * LL + i) * 512), 16,
-                                             (int)(in ? xoff[h][i] : kOut), t * 128, 0, 0);
+                                             (int)(in ? xoff[h][i] + (uint32_t)t * 128u : kOut), 0,
+                                             0, 0);
   };
   auto load_b = [&](uint16_t* dst, int h, int t, int i) __attribute__((always_inline)) {
     const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[h], (lds_void*)(dst + (wave * LL + i) * 512), 16,
-                                             (int)(in ? woff[i] : kOut), t * 128, 0, 0);
+                                             (int)(in ? woff[i] + (uint32_t)t * 128u : kOut), 0, 0,
+                                             0);
   };
 
   // Operands of part s: row lane & 15 of a block of 16, block lane / 16 + 4 s
