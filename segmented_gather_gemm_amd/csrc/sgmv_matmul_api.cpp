@@ -68,10 +68,11 @@ bool tiled_fits(const sgmv::MatmulParams& p) {
 // of large tiles is taken as 100; of medium ones as 34 with one workgroup per
 // compute unit, 57 with two, and 75 past two rounds, where their twice as
 // many bytes per product bind (measured: dense, hidden 4096, 4096 columns,
-// 4096 rows 105.6 us on 256 large tiles and 120.1 us on 1024 medium ones, 2048
-// rows 84.5 and 60.6 us, 512 rows 79.8 and 30.2 us; grouped, 8 experts x 1024
-// rows, hidden 14336, 955 and 1197 us, 32 experts x 188 rows 133.3 and 119.8
-// us).  A segment fills half of its last tile on average.
+// 4096 rows 98 us on 256 large tiles and 115 us on 1024 medium ones, 2048 rows
+// 79 and 60 us, 512 rows 72 and 32 us; grouped, 8 experts x 1024 rows, hidden
+// 14336, 885 and 1130 us, 64 experts x 32 rows 164 and 151 us; where they are
+// near each other, 32 experts x 188 rows 115 and 119 us, it may miss by 5%).  A
+// segment fills half of its last tile on average.
 sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int cus) {
   const sgmv::TiledKernel l = sgmv::matmul_tiled_large(wd, mode);
   const sgmv::TiledKernel m = sgmv::matmul_tiled_medium(wd, mode);
@@ -97,8 +98,9 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
     // up to 32 rows (64 with adapters, whose share its waves divide), and
     // segments of up to 16 rows whose 128 x 128 tiles leave half of the compute
     // units idle (hidden 4096, 4096 columns: 17 rows 11.4 us against 26.5 in
-    // medium tiles, 64 rows 25.4 and 27.1; with more columns the tiles win, 14336
-    // and 64 rows 49.0 and 28.5 us; 8 experts x 4 rows 20.9 and 18.2 us).
+    // medium tiles; 64 rows without adapters are even, 25.4 and 27.1, and with
+    // 14336 columns the tiles win, 49.0 and 28.5 us; with 32 adapters the
+    // waves' 50 us beat the tiles' 83; 8 experts x 4 rows 20.9 and 18.2 us).
     const TiledKernel m = matmul_tiled_medium(wd, mode);
     const int64_t few = 32 * (p.num_slices > 0 ? 2 : 1);
     const int64_t used = p.batches < p.T ? p.batches : p.T;

@@ -25,13 +25,13 @@
 // arrived, for every wave) and before part 0 (every wave has read it).
 //
 // What bounds it: with 256 x 256 tiles the matrix instructions (busy 77% of the
-// compute units' time at 8192 x 8192 x 8192: 770 us, 1427 TFLOP/s; the rest is
+// compute units' time at 8192 x 8192 x 8192, 740 us, 1490 TFLOP/s; the rest is
 // barriers and the tiles' first and last steps); before loads had more
 // than one step to arrive, the loads did (884 us).  Prefill of 16384 tokens,
-// hidden 4096 -> 28672: 2741 us = 1404 TFLOP/s, with 64 adapters of rank 64
-// 3045 us.  The 128 x 128 tile moves twice the bytes per product and wins
-// where the large one leaves compute units idle (512 x 4096 x 4096: 30 us
-// against 80) and for experts with few rows, which it reads at 3.4 TB/s.
+// hidden 4096 -> 28672: 2696 us = 1427 TFLOP/s, with 64 adapters of rank 64
+// 3050-3120 us.  The 128 x 128 tile moves twice the bytes per product and wins
+// where the large one leaves compute units idle (512 x 4096 x 4096: 32 us
+// against 72) and for experts with few rows, which it reads at 3.5 TB/s.
 #pragma once
 
 #include <type_traits>
