@@ -299,8 +299,12 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // Which adapters the tile's rows have, while the first loads are on their way.
   __shared__ int32_t row_pos[MODE == kAdapted ? S::BM : 1], list[MODE == kAdapted ? S::BM : 1];
   __shared__ int32_t segs[MODE == kAdapted ? 3 * S::BM : 1], count[2], odd_found;
-  if constexpr (MODE == kAdapted)
+  if constexpr (MODE == kAdapted) {
+    // Cleared ahead of tile_adapters' barriers: a tile whose columns no slice
+    // covers meets no other one before the flag is read.
+    if (threadIdx.x == 0) odd_found = 0;
     tile_adapters<S::kNT, S::BM>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
+  }
   wait_loads<kLoads>();
   wg_barrier();
 #pragma unroll
@@ -346,7 +350,6 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   if constexpr (MODE == kAdapted) {
     const int adapters = uniform(count[0]);
     constexpr int kA = S::BM * 8 / S::kNT, kB = S::BN * 8 / S::kNT;  // blocks per thread
-    if (tid == 0) odd_found = 0;
     // Width of an adapter in a step, log2 of 8 elements, and adapters a step.
     const int wide = p.K <= 8 ? 0 : p.K <= 16 ? 1 : p.K <= 32 ? 2 : 3, side = 8 >> wide;
     int mine[2 * FM];

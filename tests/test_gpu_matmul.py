@@ -128,6 +128,21 @@ def test_lora_linear_windows_with_gaps(T):
     lora_case(T, 136, [40, 24], 8, 2, [T], [1], gaps=(72, 104), seed=T)
 
 
+@pytest.mark.parametrize("T,K,widths,gaps", [(130, 8, [40, 24], (500, 400)), (300, 40, [16], (1000,)),
+                                             (3900, 16, [40, 24], (2000, 2032)), (3900, 80, [64], (4032,))])
+def test_lora_linear_windows_that_leave_tiles_without_a_slice(T, K, widths, gaps):
+    """Whole tiles of columns (128 and 256 wide) that no slice covers, under rows with adapters, after a
+    call whose weights are not finite in every tile."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T + K)
+    N = sum(widths) + sum(gaps)
+    lb = torch.full((2, N, 8), float("nan"), dtype=BF16, device="cuda")
+    o = torch.zeros(T, N, dtype=BF16, device="cuda")
+    sg.sgmv_lora_linear(normal(gen, T, 64), normal(gen, N, 64), [(normal(gen, 2, 8, 64), lb, 0)], o, i64([0]), i64([T]),
+                        i64([1]), 1, T)
+    lora_case(T, 136, widths, K, 3, [T // 2, 5, T // 3], [2, -1, 0], gaps=gaps, seed=T + K)
+
+
 @pytest.mark.parametrize("T", [12, 260])
 def test_lora_linear_nan_rows_stay_where_they_are(T):
     """NaN and infinities of one row reach that row alone; rows of the workspace that no segment
