@@ -131,13 +131,15 @@ __device__ __forceinline__ TileLoc find_tile(const MatmulParams& p, int32_t tile
 // Adapters of a tile's rows.
 // ---------------------------------------------------------------------------
 
-// Fill list[0 .. *count) with the distinct adapters of rows row0 .. end, in
-// any order, and row_pos[0 .. ROWS) with the place of row row0 + i's adapter in
-// it (-1: none) (all NT threads take
-// part, NT >= ROWS; `segs` holds 3 ROWS words, `count` two; `mine` from
-// read_segment, which a caller can issue earlier).  Segments are disjoint, so
-// at most ROWS of them meet the tile; more (a broken precondition) are
-// dropped.
+// Fill list[0 .. *count) with the distinct adapters of rows row0 .. end in
+// order of their first row, and row_pos[0 .. ROWS) with the place of row
+// row0 + i's adapter in it (-1: none) (all NT threads take part, NT >= ROWS;
+// `segs` holds adapter_words<ROWS>() words, `count` two; `mine` from
+// read_segment, which a caller can issue earlier).  The segments meet in an
+// order that changes from run to run; the few-rows kernel rounds by an
+// adapter's place, so the list's order goes by the rows.  Segments are
+// disjoint, so at most ROWS of them meet the tile; more (a broken
+// precondition) are dropped.
 struct Segment {
   int64_t start, len, a;
 };
@@ -145,13 +147,20 @@ __device__ __forceinline__ Segment read_segment(const MatmulParams& p, int32_t b
   return b < p.batches ? Segment{p.start[b], p.lens[b], p.idx[b]} : Segment{0, 0, -1};
 }
 
+// Words of LDS in which tile_adapters keeps the segments it meets.
+template <int ROWS>
+constexpr int adapter_words() { return 3 * ROWS + (ROWS + 31) / 32; }
+
 template <int NT, int ROWS>
 __device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg, int32_t row0,
                                               int32_t end, int32_t* row_pos, int32_t* list,
                                               int32_t* count, int32_t* segs) {
   static_assert(NT >= ROWS, "one row per thread");
+  constexpr int kHeads = (ROWS + 31) / 32;
+  int32_t* heads = segs + 3 * ROWS;  // a bit for every row that is some adapter's first
   const int tid = threadIdx.x;
   if (tid < 2) count[tid] = 0;
+  if (tid < kHeads) heads[tid] = 0;
   __syncthreads();
   for (int32_t b = tid; b < p.batches; b += NT) {
     if (b >= NT) seg = read_segment(p, b);
@@ -166,17 +175,36 @@ __device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg
   }
   __syncthreads();
   const int n = count[1] < ROWS ? count[1] : ROWS;
+  int32_t head = -1;  // of the adapter that this thread lists
   if (tid < ROWS) {
-    int32_t mine = -1;
-    for (int i = 0; i < n; ++i)
-      mine = segs[i] <= tid && tid < segs[ROWS + i] ? segs[2 * ROWS + i] : mine;
-    row_pos[tid] = mine;
-    if (tid < n) {  // an adapter is listed for its first segment here
-      const int32_t a = segs[2 * ROWS + tid];
-      bool first = true;
-      for (int i = 0; i < tid; ++i) first = first && segs[2 * ROWS + i] != a;
-      if (first) list[atomicAdd(&count[0], 1)] = a;
+    int32_t mine = -1;  // the row's adapter
+    // Thread i also has segment i: its adapter is listed at its first segment here.
+    const int32_t a = tid < n ? segs[2 * ROWS + tid] : -1, row = tid < n ? segs[tid] : 0;
+    bool first = tid < n;
+    for (int i = 0; i < n; ++i) {
+      const int32_t si = segs[i], ai = segs[2 * ROWS + i];
+      mine = si <= tid && tid < segs[ROWS + i] ? ai : mine;
+      first = first && (ai != a || si >= row);
     }
+    row_pos[tid] = mine;
+    if (first) {
+      head = row;
+      atomicOr(&heads[row >> 5], (int32_t)(1u << (row & 31)));
+    }
+  }
+  __syncthreads();
+  if (tid == 0 || head >= 0) {
+    int32_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const uint32_t h = (uint32_t)heads[i];
+      const int below = head - 32 * i;  // rows of this word ahead of this thread's
+      const uint32_t mask = below <= 0 ? 0u : below >= 32 ? ~0u : (1u << below) - 1u;
+      before += __builtin_popcount(h & mask);
+      all += __builtin_popcount(h);
+    }
+    if (head >= 0) list[before] = segs[2 * ROWS + tid];
+    if (tid == 0) count[0] = all;
   }
   __syncthreads();
   if (tid < ROWS) {

@@ -15,7 +15,8 @@ namespace dev {
 template <int WD, bool GATED>
 __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   __shared__ int32_t sh[kWaves + 4];
-  __shared__ int32_t row_pos[kGenericRows], list[kGenericRows], segs[3 * kGenericRows], count[2];
+  __shared__ int32_t row_pos[kGenericRows], list[kGenericRows];
+  __shared__ int32_t segs[adapter_words<kGenericRows>()], count[2];
   constexpr int kBlocks = kGenericCols / 16;
   const TileLoc loc = find_tile<kThreads>(p, kGenericRows, sh);
   if (loc.row < 0) return;

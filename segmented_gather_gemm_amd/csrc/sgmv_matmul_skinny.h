@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
   for (int g = 0; g < G; ++g) load(g, g);
   // Which adapters the tile's rows have, while the first loads are on their way.
   __shared__ int32_t row_pos[MODE == kAdapted ? ROWS : 1], list[MODE == kAdapted ? ROWS : 1];
-  __shared__ int32_t segs[MODE == kAdapted ? 3 * ROWS : 1], count[2];
+  __shared__ int32_t segs[MODE == kAdapted ? adapter_words<ROWS>() : 1], count[2];
   if constexpr (MODE == kAdapted)
     tile_adapters<kNT, ROWS>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
   for (int u = 0; u < mine; u += G) {

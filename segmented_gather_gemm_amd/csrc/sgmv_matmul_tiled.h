@@ -298,7 +298,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   for (int i = 0; i < kLoads; ++i) load_one(a10, a11, b10, b11, 1, i);
   // Which adapters the tile's rows have, while the first loads are on their way.
   __shared__ int32_t row_pos[MODE == kAdapted ? S::BM : 1], list[MODE == kAdapted ? S::BM : 1];
-  __shared__ int32_t segs[MODE == kAdapted ? 3 * S::BM : 1], count[2], odd_found;
+  __shared__ int32_t segs[MODE == kAdapted ? adapter_words<S::BM>() : 1], count[2], odd_found;
   if constexpr (MODE == kAdapted) {
     // Cleared ahead of tile_adapters' barriers: a tile whose columns no slice
     // covers meets no other one before the flag is read.

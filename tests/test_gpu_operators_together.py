@@ -101,6 +101,28 @@ def test_results_do_not_depend_on_the_run():
     assert torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2])
 
 
+@pytest.mark.parametrize("T", [16, 31, 64, 200])
+def test_results_do_not_depend_on_the_run_with_many_segments(T):
+    """Several adapters in a tile, their segments spread over a table of 1000 (most empty), so that
+    several waves find them: float32 results, the same bits every time."""
+    import segmented_gather_gemm_amd as sg
+    g = torch.Generator(device="cuda").manual_seed(T)
+    H, N, K, L, B = 520, 128, 16, 40, 1000
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(N, H, generator=g, device="cuda").to(torch.bfloat16)
+    la, lb = torch.randn(L, K, H, generator=g, device="cuda").to(torch.bfloat16), torch.randn(L, N, K, generator=g, device="cuda").to(torch.bfloat16)
+    lens, start = torch.zeros(B, dtype=torch.int64, device="cuda"), torch.zeros(B, dtype=torch.int64, device="cuda")
+    at = torch.randperm(B, generator=g, device="cuda")[:T]
+    lens[at], start[at] = 1, torch.arange(T, device="cuda")
+    idx = torch.randint(-1, L, (B,), generator=g, device="cuda")
+    first = None
+    for run in range(200):
+        o = torch.zeros(T, N, dtype=torch.float32, device="cuda")
+        sg.sgmv_lora_linear(x, w, [(la, lb, 0)], o, start, lens, idx, B, 1)
+        first = o if first is None else first
+        assert torch.equal(o, first), f"run {run}"
+
+
 def test_outputs_past_32_bit_offsets():
     """An output of more than 2^32 bytes, and gathered inputs of more than 2^31: rows from both ends."""
     import segmented_gather_gemm_amd as sg
