@@ -245,16 +245,63 @@ __device__ __forceinline__ void split_operand(const float* v, u32x4* hi, u32x4* 
   }
 }
 
-// silu(g) * u = g u / (1 + exp(-g)).  For g -> -inf exp overflows to +inf and
-// the quotient is -0; g = -inf itself gives NaN, as -inf * 0 does.
-__device__ __forceinline__ float gate(float g, float u) {
-  return g / (1.f + __expf(-g)) * u;
-}
-
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
   if (dtype == F32) return static_cast<const float*>(p)[i];
   const uint32_t h = static_cast<const uint16_t*>(p)[i];
   return dtype == BF16 ? widen<BF16>(h) : widen<F16>(h);
+}
+
+// Weights that are not finite.  The two parts of a projected value times an
+// infinity may be infinities of both signs, or zero times it, and one
+// request's weights must not reach another's rows through zeros: the kernels
+// multiply with such weights replaced by zeros, and what they add (an infinity
+// or NaN) is added to the results they belong to at the end (odd_products).
+
+// Whether any of eight packed 16-bit values is an infinity or NaN: its
+// exponent's bits are all ones, so that one more carries into the sign's place.
+template <int WD>
+__device__ __forceinline__ bool any_odd(u32x4 v) {
+  constexpr uint32_t kExp = WD == BF16 ? 0x7F807F80u : 0x7C007C00u;
+  constexpr uint32_t kOne = WD == BF16 ? 0x00800080u : 0x04000400u;
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t |= (v[i] & kExp) + kOne;
+  return (t & 0x80008000u) != 0;
+}
+
+// Those values replaced by zero.
+template <int WD>
+__device__ __forceinline__ u32x4 drop_odd(u32x4 v) {
+  constexpr uint32_t kExp = WD == BF16 ? 0x7F80u : 0x7C00u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = (v[i] & kExp) == kExp ? 0u : v[i] & 0xFFFFu;
+    const uint32_t hi = (v[i] & kExp << 16) == kExp << 16 ? 0u : v[i] & 0xFFFF0000u;
+    v[i] = hi | lo;
+  }
+  return v;
+}
+
+// What the weights of adapter a (-1: none) that are not finite add to
+// out[row][n]: 0, an infinity or NaN.
+template <int WD>
+__device__ __forceinline__ float odd_products(const MatmulParams& p, int row, int a, int n) {
+  float sum = 0.f;
+  for (int s = 0; s < p.num_slices && a >= 0; ++s) {
+    const AdapterDesc d = adapter_desc(s);
+    if (n < d.offset || n >= d.offset + d.n) continue;
+    for (int k = 0; k < p.K; ++k) {
+      const float b = load_elem(d.b, ((int64_t)a * d.n + n - d.offset) * p.K + k, WD);
+      if (!__builtin_isfinite(b)) sum += d.v[(int64_t)row * p.v_stride + k] * b;
+    }
+  }
+  return sum;
+}
+
+// silu(g) * u = g u / (1 + exp(-g)).  For g -> -inf exp overflows to +inf and
+// the quotient is -0; g = -inf itself gives NaN, as -inf * 0 does.
+__device__ __forceinline__ float gate(float g, float u) {
+  return g / (1.f + __expf(-g)) * u;
 }
 
 __device__ __forceinline__ void store_elem(void* p, int64_t i, int dtype, float v) {

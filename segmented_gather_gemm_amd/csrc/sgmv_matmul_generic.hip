@@ -16,7 +16,7 @@ template <int WD, bool GATED>
 __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   __shared__ int32_t sh[kWaves + 4];
   __shared__ int32_t row_pos[kGenericRows], list[kGenericRows];
-  __shared__ int32_t segs[adapter_words<kGenericRows>()], count[2];
+  __shared__ int32_t segs[adapter_words<kGenericRows>()], count[2], odd_found;
   constexpr int kBlocks = kGenericCols / 16;
   const TileLoc loc = find_tile<kThreads>(p, kGenericRows, sh);
   if (loc.row < 0) return;
@@ -53,7 +53,10 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
     }
   }
 
+  bool odd_weights = false;
+  int32_t adapter = -1;  // of this lane's row
   if (!GATED && p.num_slices > 0) {
+    if (threadIdx.x == 0) odd_found = 0;  // ahead of tile_adapters' barriers
     tile_adapters<kThreads, kGenericRows>(p, read_segment(p, threadIdx.x), loc.row, loc.end,
                                           row_pos, list, count, segs);
     const int32_t adapters = uniform(count[0]);
@@ -62,7 +65,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
       const int32_t a = uniform(list[i]);
       if (__ballot(my_pos == i) == 0) continue;  // none of this wave's rows
       // The sums go on from the accumulators and are kept in the lanes whose
-      // token has the adapter: its weights (a NaN, say) reach no other row.
+      // token has the adapter.
       f32x4 sum[kBlocks];
 #pragma unroll
       for (int f = 0; f < kBlocks; ++f) sum[f] = acc[0][f];
@@ -84,6 +87,10 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
             const bool in = n >= 0 && n < d.n;
             u32x4 bv;
             load_any8<WD>(d.b, ((int64_t)a * d.n + (in ? n : 0)) * p.K + at, in ? cnt : 0, vb, &bv);
+            if (any_odd<WD>(bv)) {
+              odd_found = 1;
+              bv = drop_odd<WD>(bv);
+            }
             sum[f] = mfma<WD>(bv, hi, sum[f]);
             sum[f] = mfma<WD>(bv, lo, sum[f]);
           }
@@ -94,6 +101,9 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[0][f][j] = my_pos == i ? sum[f][j] : acc[0][f][j];
     }
+    __syncthreads();
+    odd_weights = uniform(odd_found) != 0;
+    adapter = my_pos < 0 ? -1 : list[my_pos];
   }
 
   if (!live) return;
@@ -109,6 +119,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
         y = gate(acc[0][f][i], acc[1][f][i]);
       } else {
         y = acc[0][f][i];
+        if (odd_weights) y += odd_products<WD>(p, row, adapter, n);
         if (p.bias) y += load_elem(p.bias, n, WD);
         if (p.add) y += load_elem(orow, n, p.out_dtype);
       }

@@ -95,9 +95,11 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
   for (int g = 0; g < G; ++g) load(g, g);
   // Which adapters the tile's rows have, while the first loads are on their way.
   __shared__ int32_t row_pos[MODE == kAdapted ? ROWS : 1], list[MODE == kAdapted ? ROWS : 1];
-  __shared__ int32_t segs[MODE == kAdapted ? adapter_words<ROWS>() : 1], count[2];
-  if constexpr (MODE == kAdapted)
+  __shared__ int32_t segs[MODE == kAdapted ? adapter_words<ROWS>() : 1], count[2], odd_found;
+  if constexpr (MODE == kAdapted) {
+    if (threadIdx.x == 0) odd_found = 0;  // ahead of tile_adapters' barriers
     tile_adapters<kNT, ROWS>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
+  }
   for (int u = 0; u < mine; u += G) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {  // past the last step: zeros
@@ -151,6 +153,18 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
                             &bv[j][n]);
             }
           }
+          bool odd = false;
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) odd = odd || any_odd<WD>(bv[j][n]);
+          if (__ballot(odd) != 0) {
+            odd_found = 1;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+              for (int n = 0; n < NB; ++n) bv[j][n] = drop_odd<WD>(bv[j][n]);
+          }
           if (i == wave) {
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
@@ -188,6 +202,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
       for (int n = 0; n < NB; ++n)
         *reinterpret_cast<f32x4*>(&part[wave][(t * MB + m) * NB + n][lr][lq * 4]) = acc[t][m][n];
   __syncthreads();
+  [[maybe_unused]] bool odd_weights = false;
+  if constexpr (MODE == kAdapted) odd_weights = uniform(odd_found) != 0;
   for (int e = threadIdx.x; e < ROWS * 16 * NB; e += kNT) {
     const int c = e % (16 * NB), r = e / (16 * NB), n = c / 16, m = r / 16;
     const int col = n0 + c;
@@ -201,6 +217,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
     }
     char* out = static_cast<char*>(p.out) + (int64_t)(loc.row + r) * p.out_row_bytes;
     float v = MODE == kGated ? gate(y[0], y[kMats - 1]) : y[0];
+    if constexpr (MODE == kAdapted) {
+      if (odd_weights)
+        v += odd_products<WD>(p, loc.row + r, row_pos[r] < 0 ? -1 : list[row_pos[r]], col);
+    }
     if constexpr (MODE == kDense || MODE == kAdapted) {
       if (p.bias) v += load_elem(p.bias, col, WD);
       if (p.add) v += load_elem(out, col, p.out_dtype);

@@ -90,31 +90,6 @@ __device__ __forceinline__ void mfma_into(f32x4& c, u32x4 a, u32x4 b) {
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
-// Two 16-bit values with those that are not finite replaced by zero.
-template <int WD>
-__device__ __forceinline__ uint32_t finite_pair(uint32_t v) {
-  constexpr uint32_t kExp = WD == BF16 ? 0x7F80u : 0x7C00u;
-  const uint32_t lo = (v & kExp) == kExp ? 0u : v & 0xFFFFu;
-  const uint32_t hi = (v & kExp << 16) == kExp << 16 ? 0u : v & 0xFFFF0000u;
-  return hi | lo;
-}
-
-// What the weights of adapter a that are not finite add to out[row][n]: 0
-// nothing, 1 +inf, 2 -inf, 3 NaN.
-template <int WD>
-__device__ __forceinline__ uint8_t odd_products(const MatmulParams& p, int row, int a, int n) {
-  float sum = 0.f;
-  for (int s = 0; s < p.num_slices && a >= 0; ++s) {
-    const AdapterDesc d = adapter_desc(s);
-    if (n < d.offset || n >= d.offset + d.n) continue;
-    for (int k = 0; k < p.K; ++k) {
-      const float b = load_elem(d.b, ((int64_t)a * d.n + n - d.offset) * p.K + k, WD);
-      if (!__builtin_isfinite(b)) sum += d.v[(int64_t)row * p.v_stride + k] * b;
-    }
-  }
-  return sum == 0.f ? 0 : sum != sum ? 3 : sum > 0.f ? 1 : 2;
-}
-
 // Operands that other instructions wrote are there for mfma_into.
 __device__ __forceinline__ void mfma_ready() {
   pin();
@@ -386,11 +361,11 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
           for (int j = 0; j < kB; ++j) {
             const int u = tid + j * S::kNT, q = u >> 3, c = u & 7;
             uint16_t* dst = q < HN ? B0 : B1;
-            u32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = finite_pair<WD>(nb[j][i]);
-            found = found || v[0] != nb[j][0] || v[1] != nb[j][1] || v[2] != nb[j][2] ||
-                    v[3] != nb[j][3];
+            u32x4 v = nb[j];
+            if (any_odd<WD>(v)) {
+              v = drop_odd<WD>(v);
+              found = true;
+            }
             *reinterpret_cast<u32x4*>(dst + (q % HN) * 64 + ((c ^ (q & 7)) * 8)) = v;
           }
           if (found) odd_found = 1;
@@ -454,8 +429,11 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
         const int r = u / S::BN, c = u % S::BN;
         if (r < rows && n0 + c < p.N) {
           uint16_t* part = r < HM ? (r < HM / 2 ? a00 : a01) : (r < HM + HM / 2 ? a10 : a11);
-          reinterpret_cast<uint8_t*>(part)[r % (HM / 2) * S::BN + c] =
+          const float odd =
               odd_products<WD>(p, loc.row + r, row_pos[r] < 0 ? -1 : list[row_pos[r]], n0 + c);
+          // 0 nothing, 1 +inf, 2 -inf, 3 NaN
+          reinterpret_cast<uint8_t*>(part)[r % (HM / 2) * S::BN + c] =
+              odd == 0.f ? 0 : odd != odd ? 3 : odd > 0.f ? 1 : 2;
         }
       }
       __syncthreads();

@@ -360,3 +360,54 @@ def test_lora_linear_slices_without_columns(T):
         sg.sgmv_lora_linear(x, w, slices, o, i64([0]), i64([T]), i64([1]), 1, T)
         want, bound = U.lora_linear(x, w, None, [s for s in slices if s[1].shape[1]], [0], [T], [1], 1.0, o, False, BF16)
         U.assert_within(o, want, bound)
+
+
+def ieee_adapters(x, w, slices, start, lens, idx):
+    """The 64-bit sum with every product of a projected value and a weight taken by itself, so that
+    infinities and NaN come out as IEEE arithmetic gives them."""
+    y = x.double().cpu() @ w.double().cpu().t()
+    for st, n, a in zip(start, lens, idx):
+        for la, lb, off in slices if a >= 0 else ():
+            A, B = la[a].double().cpu(), lb[a].double().cpu()
+            v = (x[st:st + n].double().cpu()[:, None, :] * A[None]).sum(dim=2)
+            y[st:st + n, off:off + B.shape[0]] += (v[:, None, :] * B[None]).sum(dim=2)
+    return y
+
+
+def check_against_ieee(o, x, w, slices, start, lens, idx):
+    """Values that are not finite as in ieee_adapters; the others within the bound of the sums with the
+    weights that are not finite taken as zeros (they are multiplied by nothing there)."""
+    want = ieee_adapters(x, w, slices, start, lens, idx)
+    got, odd = o.double().cpu(), ~torch.isfinite(want)
+    clean = [(torch.nan_to_num(la, nan=0, posinf=0, neginf=0), torch.nan_to_num(lb, nan=0, posinf=0, neginf=0), off)
+             for la, lb, off in slices]
+    _, bound = U.lora_linear(x, w, None, clean, start, lens, idx, 1.0, o, False, o.dtype)
+    U.assert_within(got[~odd], want[~odd], bound[~odd])
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    inf = odd & ~torch.isnan(want)
+    assert torch.equal(got[inf], want[inf])
+    return odd
+
+
+# Few-row kernels (1 to 64 rows), both tiles, and the generic kernel (rank 13).
+ODD_SHAPES = [(1, 16), (5, 16), (16, 40), (27, 8), (50, 16), (64, 72), (5, 13), (100, 13), (100, 16), (300, 40), (3900, 16)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,K", ODD_SHAPES)
+def test_lora_linear_odd_weights_as_in_ieee(T, K, dtype):
+    """Infinities and NaN among one adapter's lora_B: an infinity times a finite value is an infinity,
+    whichever way a kernel splits the value."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T + K)
+    H, N, L = 72, 4096 if T > 1000 else 152, 3
+    x, w = normal(gen, T, H, dtype=dtype), normal(gen, N, H, sigma=H ** -0.5, dtype=dtype)
+    la, lb = normal(gen, L, K, H, sigma=H ** -0.5, dtype=dtype), normal(gen, L, N, K, dtype=dtype)
+    inf, nan = float("inf"), float("nan")
+    lb[1, 5, 3], lb[1, 9, 0], lb[1, 130, 2], lb[1, 130, 7], lb[1, 17, K - 1] = inf, nan, -inf, inf, -inf
+    x[T // 2], la[1, 3] = 1.0, 2.0 ** -3  # a value that one part of the split holds whole, the other is zero
+    start, lens, idx = [0, T // 3], [T // 3, T - T // 3], [0, 1]
+    o = torch.zeros(T, N, dtype=dtype, device="cuda")
+    sg.sgmv_lora_linear(x, w, [(la, lb, 0)], o, i64(start), i64(lens), i64(idx), 2, T)
+    odd = check_against_ieee(o, x, w, [(la, lb, 0)], start, lens, idx)
+    assert odd[T // 3:, [5, 9, 17, 130]].all() and int(odd.sum()) == 4 * (T - T // 3)
