@@ -251,11 +251,12 @@ __device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) 
   return dtype == BF16 ? widen<BF16>(h) : widen<F16>(h);
 }
 
-// Weights that are not finite.  The two parts of a projected value times an
-// infinity may be infinities of both signs, or zero times it, and one
-// request's weights must not reach another's rows through zeros: the kernels
-// multiply with such weights replaced by zeros, and what they add (an infinity
-// or NaN) is added to the results they belong to at the end (odd_products).
+// Projected values and weights that are not finite.  The two parts of a value
+// times an infinity may be infinities of both signs, or zero times it; one
+// request's weights must not reach another's rows, nor a slice's values the
+// columns outside its window, through zeros.  The kernels multiply with what
+// is not finite replaced by zeros, and what its products add (an infinity or
+// NaN) is added to the results they belong to at the end (odd_products).
 
 // Whether any of eight packed 16-bit values is an infinity or NaN: its
 // exponent's bits are all ones, so that one more carries into the sign's place.
@@ -282,8 +283,23 @@ __device__ __forceinline__ u32x4 drop_odd(u32x4 v) {
   return v;
 }
 
-// What the weights of adapter a (-1: none) that are not finite add to
-// out[row][n]: 0, an infinity or NaN.
+// The same for eight float32 values.
+__device__ __forceinline__ bool any_odd(const float* v) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    most = m > most ? m : most;
+  }
+  return most >= 0x7F800000u;
+}
+__device__ __forceinline__ void drop_odd(float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __builtin_isfinite(v[i]) ? v[i] : 0.f;
+}
+
+// What the products that are not finite, of row `row`'s values with the weights
+// of adapter a (-1: none), add to out[row][n]: 0, an infinity or NaN.
 template <int WD>
 __device__ __forceinline__ float odd_products(const MatmulParams& p, int row, int a, int n) {
   float sum = 0.f;
@@ -292,7 +308,8 @@ __device__ __forceinline__ float odd_products(const MatmulParams& p, int row, in
     if (n < d.offset || n >= d.offset + d.n) continue;
     for (int k = 0; k < p.K; ++k) {
       const float b = load_elem(d.b, ((int64_t)a * d.n + n - d.offset) * p.K + k, WD);
-      if (!__builtin_isfinite(b)) sum += d.v[(int64_t)row * p.v_stride + k] * b;
+      const float v = d.v[(int64_t)row * p.v_stride + k];
+      if (!__builtin_isfinite(b) || !__builtin_isfinite(v)) sum += v * b;
     }
   }
   return sum;

@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
     }
   }
 
-  bool odd_weights = false;
+  bool odd_values = false;
   int32_t adapter = -1;  // of this lane's row
   if (!GATED && p.num_slices > 0) {
     if (threadIdx.x == 0) odd_found = 0;  // ahead of tile_adapters' barriers
@@ -79,6 +79,10 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             v[j] = live && j < cnt ? d.v[(int64_t)row * p.v_stride + at + j] : 0.f;
+          if (any_odd(v)) {
+            drop_odd(v);
+            if (my_pos >= 0) odd_found = 1;  // else no segment's row: anything may be there
+          }
           u32x4 hi, lo;
           split_operand<WD>(v, &hi, &lo);
 #pragma unroll
@@ -102,7 +106,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
         for (int j = 0; j < 4; ++j) acc[0][f][j] = my_pos == i ? sum[f][j] : acc[0][f][j];
     }
     __syncthreads();
-    odd_weights = uniform(odd_found) != 0;
+    odd_values = uniform(odd_found) != 0;
     adapter = my_pos < 0 ? -1 : list[my_pos];
   }
 
@@ -119,7 +123,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
         y = gate(acc[0][f][i], acc[1][f][i]);
       } else {
         y = acc[0][f][i];
-        if (odd_weights) y += odd_products<WD>(p, row, adapter, n);
+        if (odd_values) y += odd_products<WD>(p, row, adapter, n);
         if (p.bias) y += load_elem(p.bias, n, WD);
         if (p.add) y += load_elem(orow, n, p.out_dtype);
       }

@@ -170,6 +170,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
             for (int m = 0; m < MB; ++m) {
               float v[8];
               out_values<F32>(raw[m], v);
+              if (any_odd(v)) {
+                drop_odd(v);
+                if (pos[m] >= 0) odd_found = 1;  // else no segment's row: anything may be there
+              }
               split_operand<WD>(v, &hi[m], &lo[m]);
             }
           }
@@ -202,8 +206,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
       for (int n = 0; n < NB; ++n)
         *reinterpret_cast<f32x4*>(&part[wave][(t * MB + m) * NB + n][lr][lq * 4]) = acc[t][m][n];
   __syncthreads();
-  [[maybe_unused]] bool odd_weights = false;
-  if constexpr (MODE == kAdapted) odd_weights = uniform(odd_found) != 0;
+  [[maybe_unused]] bool odd_values = false;
+  if constexpr (MODE == kAdapted) odd_values = uniform(odd_found) != 0;
   for (int e = threadIdx.x; e < ROWS * 16 * NB; e += kNT) {
     const int c = e % (16 * NB), r = e / (16 * NB), n = c / 16, m = r / 16;
     const int col = n0 + c;
@@ -218,7 +222,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
     char* out = static_cast<char*>(p.out) + (int64_t)(loc.row + r) * p.out_row_bytes;
     float v = MODE == kGated ? gate(y[0], y[kMats - 1]) : y[0];
     if constexpr (MODE == kAdapted) {
-      if (odd_weights)
+      if (odd_values)
         v += odd_products<WD>(p, loc.row + r, row_pos[r] < 0 ? -1 : list[row_pos[r]], col);
     }
     if constexpr (MODE == kDense || MODE == kAdapted) {

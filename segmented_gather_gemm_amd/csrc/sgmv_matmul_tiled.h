@@ -318,10 +318,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // 32 put 8, 4 and 2 adapters side by side into a step of 64, so that a tile
   // of many single-token requests takes fewer of them.  A row takes
   // part with its own adapter and with zeros elsewhere; so that zero times
-  // what another request's weights hold is nothing, weights that are not
-  // finite are staged as zeros here and their products are added at the end,
-  // to the rows that have them.
-  [[maybe_unused]] bool odd_weights = false;
+  // what another request's weights or another slice's rows hold is nothing,
+  // what is not finite is staged as zeros here and its products are added at
+  // the end, where they belong.
+  [[maybe_unused]] bool odd_values = false;
   if constexpr (MODE == kAdapted) {
     const int adapters = uniform(count[0]);
     constexpr int kA = S::BM * 8 / S::kNT, kB = S::BN * 8 / S::kNT;  // blocks per thread
@@ -380,6 +380,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
           buf_load8<F32>(vr, at < p.K ? (uint32_t)(r * p.v_stride + at) * 4u : kOut, raw);
           float v[8];
           out_values<F32>(raw, v);
+          if (any_odd(v)) {
+            drop_odd(v);
+            if (row_pos[r] >= 0) odd_found = 1;  // else no segment's row: anything may be there
+          }
           split_operand<WD>(v, &hi, &lo);
           const int to = (r % HM) * 64 + ((c ^ (r & 7)) * 8);
           *reinterpret_cast<u32x4*>((r < HM ? a00 : a01) + to) = hi;
@@ -422,8 +426,8 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
         }
       }
     }
-    odd_weights = adapters > 0 && uniform(odd_found) != 0;
-    if (odd_weights) {  // the A buffers, free now, take a code for every result
+    odd_values = adapters > 0 && uniform(odd_found) != 0;
+    if (odd_values) {  // the A buffers, free now, take a code for every result
 #pragma unroll 1
       for (int u = tid; u < S::BM * S::BN; u += S::kNT) {
         const int r = u / S::BN, c = u % S::BN;
@@ -479,7 +483,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
                                     : acc[h][bh][m][f][j & 3] + bias[j];
             }
             if constexpr (MODE == kAdapted) {
-              if (odd_weights) {
+              if (odd_values) {
                 const uint16_t* half = h == 0 ? (r < HM / 2 ? a00 : a01)
                                               : (r < HM + HM / 2 ? a10 : a11);
                 const uint2 codes = *reinterpret_cast<const uint2*>(

@@ -411,3 +411,30 @@ def test_lora_linear_odd_weights_as_in_ieee(T, K, dtype):
     sg.sgmv_lora_linear(x, w, [(la, lb, 0)], o, i64(start), i64(lens), i64(idx), 2, T)
     odd = check_against_ieee(o, x, w, [(la, lb, 0)], start, lens, idx)
     assert odd[T // 3:, [5, 9, 17, 130]].all() and int(odd.sum()) == 4 * (T - T // 3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,K", ODD_SHAPES)
+def test_lora_linear_odd_projections_stay_in_their_window(T, K, dtype):
+    """Projected values that are not finite (from lora_A) in the first of three slices: they reach its
+    columns, in the rows that have the adapter, as IEEE arithmetic says (times 0: NaN), and neither the
+    other slices' columns nor the gap between them, which lie in the same tile."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T + K)
+    H, L = 72, 3
+    widths, offs, N = [40, 24, 32], [0, 40, 80], 4096 if T > 1000 else 152
+    x, w = normal(gen, T, H, dtype=dtype), normal(gen, N, H, sigma=H ** -0.5, dtype=dtype)
+    slices = [(normal(gen, L, K, H, sigma=H ** -0.5, dtype=dtype), normal(gen, L, n, K, dtype=dtype), off)
+              for n, off in zip(widths, offs)]
+    la, lb, _ = slices[0]
+    inf, nan = float("inf"), float("nan")
+    la[1, 0, 7], la[2, K - 1, 3] = inf, nan
+    x[:, 7] = x[:, 7].abs() + 0.5
+    lb[1, 3, 0], lb[1, 11, 0], lb[1, 12, 0] = 0.0, inf, -inf
+    lens = [T // 4, T // 4, T // 4, T - 3 * (T // 4)]
+    start, idx = [0, lens[0], 2 * lens[0], 3 * lens[0]], [0, 2, -1, 1]
+    o = torch.zeros(T, N, dtype=dtype, device="cuda")
+    sg.sgmv_lora_linear(x, w, slices, o, i64(start), i64(lens), i64(idx), 4, T)
+    odd = check_against_ieee(o, x, w, slices, start, lens, idx)
+    rows = list(range(start[1], start[2])) + list(range(start[3], T))
+    assert odd[rows, :40].all() and int(odd.sum()) == 40 * len(rows)
