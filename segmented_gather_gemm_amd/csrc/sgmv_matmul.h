@@ -131,14 +131,16 @@ __device__ __forceinline__ TileLoc find_tile(const MatmulParams& p, int32_t tile
 // Adapters of a tile's rows.
 // ---------------------------------------------------------------------------
 
-// Fill list[0 .. *count) with the distinct adapters of rows row0 .. end in
-// order of their first row, and row_pos[0 .. ROWS) with the place of row
-// row0 + i's adapter in it (-1: none) (all NT threads take part, NT >= ROWS;
-// `segs` holds adapter_words<ROWS>() words, `count` two; `mine` from
-// read_segment, which a caller can issue earlier).  The segments meet in an
-// order that changes from run to run; the few-rows kernel rounds by an
-// adapter's place, so the list's order goes by the rows.  Segments are
-// disjoint, so at most ROWS of them meet the tile; more (a broken
+// Fill list[0 .. *count) with the distinct adapters of rows row0 .. end and
+// row_pos[0 .. ROWS) with the place of row row0 + i's adapter in it (-1: none)
+// (all NT threads take part, NT >= ROWS; `segs` holds adapter_words<ROWS>()
+// words, `count` two; `mine` from read_segment, which a caller can issue
+// earlier).  The segments meet in an order that changes from run to run.
+// ORDERED lists the adapters in order of their first row, for the kernel whose
+// rounding goes by an adapter's place (few rows); in the others an adapter's
+// products meet zeros, whatever stands beside them, and the order by rows
+// would cost 1% of a large prefill (256 rows, gate/up 2998 -> 3033 us).
+// Segments are disjoint, so at most ROWS of them meet the tile; more (a broken
 // precondition) are dropped.
 struct Segment {
   int64_t start, len, a;
@@ -151,7 +153,7 @@ __device__ __forceinline__ Segment read_segment(const MatmulParams& p, int32_t b
 template <int ROWS>
 constexpr int adapter_words() { return 3 * ROWS + (ROWS + 31) / 32; }
 
-template <int NT, int ROWS>
+template <int NT, int ROWS, bool ORDERED>
 __device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg, int32_t row0,
                                               int32_t end, int32_t* row_pos, int32_t* list,
                                               int32_t* count, int32_t* segs) {
@@ -160,7 +162,7 @@ __device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg
   int32_t* heads = segs + 3 * ROWS;  // a bit for every row that is some adapter's first
   const int tid = threadIdx.x;
   if (tid < 2) count[tid] = 0;
-  if (tid < kHeads) heads[tid] = 0;
+  if (ORDERED && tid < kHeads) heads[tid] = 0;
   __syncthreads();
   for (int32_t b = tid; b < p.batches; b += NT) {
     if (b >= NT) seg = read_segment(p, b);
@@ -187,13 +189,14 @@ __device__ __forceinline__ void tile_adapters(const MatmulParams& p, Segment seg
       first = first && (ai != a || si >= row);
     }
     row_pos[tid] = mine;
-    if (first) {
+    if (first && !ORDERED) list[atomicAdd(&count[0], 1)] = a;
+    if (first && ORDERED) {
       head = row;
       atomicOr(&heads[row >> 5], (int32_t)(1u << (row & 31)));
     }
   }
-  __syncthreads();
-  if (tid == 0 || head >= 0) {
+  if (ORDERED) __syncthreads();
+  if (ORDERED && (tid == 0 || head >= 0)) {
     int32_t before = 0, all = 0;
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   int32_t adapter = -1;  // of this lane's row
   if (!GATED && p.num_slices > 0) {
     if (threadIdx.x == 0) odd_found = 0;  // ahead of tile_adapters' barriers
-    tile_adapters<kThreads, kGenericRows>(p, read_segment(p, threadIdx.x), loc.row, loc.end,
+    tile_adapters<kThreads, kGenericRows, false>(p, read_segment(p, threadIdx.x), loc.row, loc.end,
                                           row_pos, list, count, segs);
     const int32_t adapters = uniform(count[0]);
     const int32_t my_pos = row_pos[wave * 16 + (lane & 15)];

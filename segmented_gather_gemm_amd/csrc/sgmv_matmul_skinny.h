@@ -98,7 +98,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
   __shared__ int32_t segs[MODE == kAdapted ? adapter_words<ROWS>() : 1], count[2], odd_found;
   if constexpr (MODE == kAdapted) {
     if (threadIdx.x == 0) odd_found = 0;  // ahead of tile_adapters' barriers
-    tile_adapters<kNT, ROWS>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
+    tile_adapters<kNT, ROWS, true>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
   }
   for (int u = 0; u < mine; u += G) {
 #pragma unroll

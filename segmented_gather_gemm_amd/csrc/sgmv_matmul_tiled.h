@@ -278,7 +278,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     // Cleared ahead of tile_adapters' barriers: a tile whose columns no slice
     // covers meets no other one before the flag is read.
     if (threadIdx.x == 0) odd_found = 0;
-    tile_adapters<S::kNT, S::BM>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
+    tile_adapters<S::kNT, S::BM, false>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
   }
   wait_loads<kLoads>();
   wg_barrier();
