@@ -230,10 +230,11 @@ __device__ __forceinline__ AdapterDesc adapter_desc(int i) {
   return AdapterDesc{d.b, d.v, d.n, d.offset};
 }
 
-// Eight float32 values as two packed operands of the 16-bit weight dtype,
-// v = hi + lo to 16 (bfloat16) or 22 (float16) bits: one rounding to the
+// Eight finite float32 values as two packed operands of the 16-bit weight
+// dtype, v = hi + lo to 16 (bfloat16) or 22 (float16) bits: one rounding to the
 // weights' dtype would leave the adapters' share of a float32 result with an
-// error of 2^-9 or 2^-12.  A value past float16's range becomes an infinity.
+// error of 2^-9 or 2^-12.  float16 has these bits from 2^-2 to 2^15 only (lo
+// ends at 2^-24, hi at 65504): see split_exponent.
 template <int WD>
 __device__ __forceinline__ void split_operand(const float* v, u32x4* hi, u32x4* lo) {
 #pragma unroll
@@ -246,6 +247,33 @@ __device__ __forceinline__ void split_operand(const float* v, u32x4* hi, u32x4* 
     (*hi)[i] = h;
     (*lo)[i] = pack2<WD>(r0, r1);
   }
+}
+
+// float16: the e for which a row's values times 2^e have 22 bits of the largest
+// in two parts, from the bits of its magnitude.  0 where they have them as they
+// are, which is the usual case; else the largest comes to lie at 2^14, or, of
+// values below 2^-26, 2^40 times higher.  The products are multiplied by 2^-e
+// again, both exact.
+__device__ __forceinline__ int split_exponent(uint32_t largest) {
+  const int x = (int)(largest >> 23) - 127;
+  return largest == 0 || (x >= -2 && x < 15) ? 0 : x < -26 ? 40 : 14 - x;
+}
+
+// Bits of the largest magnitude of eight values.
+__device__ __forceinline__ uint32_t largest_of(const float* v) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    most = m > most ? m : most;
+  }
+  return most;
+}
+
+// Eight values times 2^e.
+__device__ __forceinline__ void scale_values(float* v, int e) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = ldexpf(v[i], e);
 }
 
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
@@ -287,15 +315,8 @@ __device__ __forceinline__ u32x4 drop_odd(u32x4 v) {
 }
 
 // The same for eight float32 values.
-__device__ __forceinline__ bool any_odd(const float* v) {
-  uint32_t most = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-    most = m > most ? m : most;
-  }
-  return most >= 0x7F800000u;
-}
+constexpr uint32_t kOddBits = 0x7F800000u;  // the least magnitude's that is not finite
+__device__ __forceinline__ bool any_odd(const float* v) { return largest_of(v) >= kOddBits; }
 __device__ __forceinline__ void drop_odd(float* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __builtin_isfinite(v[i]) ? v[i] : 0.f;

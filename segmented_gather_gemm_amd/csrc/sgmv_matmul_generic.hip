@@ -65,7 +65,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
       const int32_t a = uniform(list[i]);
       if (__ballot(my_pos == i) == 0) continue;  // none of this wave's rows
       // The sums go on from the accumulators and are kept in the lanes whose
-      // token has the adapter.
+      // token has the adapter.  float16 adds each step's products times 2^-e.
       f32x4 sum[kBlocks];
 #pragma unroll
       for (int f = 0; f < kBlocks; ++f) sum[f] = acc[0][f];
@@ -83,6 +83,15 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
             drop_odd(v);
             if (my_pos >= 0) odd_found = 1;  // else no segment's row: anything may be there
           }
+          int e = 0;
+          if constexpr (WD == F16) {  // a token's 32 values are in four lanes
+            uint32_t most = largest_of(v);
+            uint32_t other = (uint32_t)__shfl_xor((int)most, 16);
+            most = other > most ? other : most;
+            other = (uint32_t)__shfl_xor((int)most, 32);
+            e = split_exponent(other > most ? other : most);
+            scale_values(v, e);
+          }
           u32x4 hi, lo;
           split_operand<WD>(v, &hi, &lo);
 #pragma unroll
@@ -95,8 +104,10 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
               odd_found = 1;
               bv = drop_odd<WD>(bv);
             }
-            sum[f] = mfma<WD>(bv, hi, sum[f]);
-            sum[f] = mfma<WD>(bv, lo, sum[f]);
+            f32x4 d = mfma<WD>(bv, hi, WD == F16 ? f32x4{} : sum[f]);
+            d = mfma<WD>(bv, lo, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[f][j] = WD == F16 ? sum[f][j] + ldexpf(d[j], -e) : d[j];
           }
         }
       }

@@ -134,6 +134,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
       for (int k = 0; k < p.K; k += 32) {
         const int at = k + lq * 8;
         u32x4 raw[MB][2], hi[MB], lo[MB];
+        [[maybe_unused]] int e[MB];  // float16: exponent of a token's values in the parts
 #pragma unroll
         for (int m = 0; m < MB; ++m)
           buf_load8<F32>(vr, at < p.K ? (uint32_t)((m * 16 + lr) * p.v_stride + at) * 4u : kOut,
@@ -174,6 +175,14 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
                 drop_odd(v);
                 if (pos[m] >= 0) odd_found = 1;  // else no segment's row: anything may be there
               }
+              if constexpr (WD == F16) {  // a token's 32 values are in the lanes lr + 16 q
+                uint32_t most = largest_of(v);
+                uint32_t other = (uint32_t)__shfl_xor((int)most, 16);
+                most = other > most ? other : most;
+                other = (uint32_t)__shfl_xor((int)most, 32);
+                e[m] = split_exponent(other > most ? other : most);
+                scale_values(v, e[m]);
+              }
               split_operand<WD>(v, &hi[m], &lo[m]);
             }
           }
@@ -189,7 +198,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
                 f32x4 d = mfma<WD>(bv[j][n], hi[m], f32x4{});
                 d = mfma<WD>(bv[j][n], lo[m], d);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[0][m][n][q] += own ? d[q] : 0.f;
+                for (int q = 0; q < 4; ++q) {
+                  const float y = WD == F16 ? ldexpf(d[q], -e[m]) : d[q];
+                  acc[0][m][n][q] += own ? y : 0.f;
+                }
               }
             }
           }

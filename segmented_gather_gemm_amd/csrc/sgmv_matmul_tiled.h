@@ -90,6 +90,14 @@ __device__ __forceinline__ void mfma_into(f32x4& c, u32x4 a, u32x4 b) {
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
+// The larger of a lane's value and the one that DPP control CTRL (of all lanes'
+// exchange) brings it.
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_max(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+  return o > v ? o : v;
+}
+
 // Operands that other instructions wrote are there for mfma_into.
 __device__ __forceinline__ void mfma_ready() {
   pin();
@@ -274,10 +282,16 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // Which adapters the tile's rows have, while the first loads are on their way.
   __shared__ int32_t row_pos[MODE == kAdapted ? S::BM : 1], list[MODE == kAdapted ? S::BM : 1];
   __shared__ int32_t segs[MODE == kAdapted ? adapter_words<S::BM>() : 1], count[2], odd_found;
+  // float16: exponent 2 e of the values of a row that are staged (and of its
+  // accumulators), bit 0 set once e was below zero; and e less the one before.
+  constexpr bool kScaled = MODE == kAdapted && WD == F16;
+  __shared__ int32_t row_exp[kScaled ? S::BM : 1], row_step[kScaled ? S::BM : 1], any_scaled;
   if constexpr (MODE == kAdapted) {
     // Cleared ahead of tile_adapters' barriers: a tile whose columns no slice
     // covers meets no other one before the flag is read.
     if (threadIdx.x == 0) odd_found = 0;
+    if (kScaled && threadIdx.x < S::BM) row_exp[threadIdx.x] = row_step[threadIdx.x] = 0;
+    if (kScaled && threadIdx.x == 0) any_scaled = 0;
     tile_adapters<S::kNT, S::BM, false>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
   }
   wait_loads<kLoads>();
@@ -331,6 +345,34 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
 #pragma unroll
     for (int m = 0; m < 2 * FM; ++m)
       mine[m] = row_pos[(m / FM) * HM + (wm * FM + m % FM) * 16 + erow];
+    [[maybe_unused]] bool scaled = false;  // some row had an exponent but 0
+    // The accumulators of row r times 2^step(r), where any of the wave's rows
+    // takes another exponent.
+    auto rescale = [&](auto step) __attribute__((always_inline)) {
+      int by[2 * FM];
+      bool any = false;
+#pragma unroll
+      for (int m = 0; m < 2 * FM; ++m) {
+        by[m] = step((m / FM) * HM + (wm * FM + m % FM) * 16 + erow);
+        any = any || by[m] != 0;
+      }
+      if (__ballot(any) == 0) return;
+      mfma_done();
+#pragma unroll
+      for (int m = 0; m < 2 * FM; ++m)
+#pragma unroll
+        for (int n = 0; n < 2 * FN; ++n) {
+          // The copy is made here and goes back before the next one's: the
+          // compiler would hold all of them in vector registers otherwise.
+          f32x4& c = acc[m / FM][n / FN][m % FM][n % FN];
+          asm volatile("" : "+a"(c));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[j] = ldexpf(c[j], by[m]);
+          asm volatile("" : "+a"(c));
+          pin();
+        }
+      mfma_ready();
+    };
     for (int sl = 0; sl < (adapters > 0 ? p.num_slices : 0); ++sl) {
       const AdapterDesc d = adapter_desc(sl);
       if (d.offset >= n0 + S::BN || d.offset + d.n <= n0) continue;
@@ -372,25 +414,73 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
         };
         load_lora_b(0);
         __syncthreads();  // the LDS is free: last step's or last round's reads are over
+        float v[kA][8];  // all loads ahead of the branches below: they arrive together
+        uint32_t most[kA], worst = 0;
 #pragma unroll
         for (int j = 0; j < kA; ++j) {
           const int u = tid + j * S::kNT, r = u >> 3, c = u & 7;
-          u32x4 raw[2], hi, lo;
+          u32x4 raw[2];
           const int at = k + ((c & ((1 << wide) - 1)) << 3);
           buf_load8<F32>(vr, at < p.K ? (uint32_t)(r * p.v_stride + at) * 4u : kOut, raw);
-          float v[8];
-          out_values<F32>(raw, v);
-          if (any_odd(v)) {
-            drop_odd(v);
-            if (row_pos[r] >= 0) odd_found = 1;  // else no segment's row: anything may be there
+          out_values<F32>(raw, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+          most[j] = largest_of(v[j]);
+          worst = most[j] > worst ? most[j] : worst;
+        }
+        if (worst >= kOddBits) {
+#pragma unroll
+          for (int j = 0; j < kA; ++j) {
+            // a row of no segment may hold anything
+            if (most[j] >= kOddBits && row_pos[(tid + j * S::kNT) >> 3] >= 0) odd_found = 1;
+            drop_odd(v[j]);
+            most[j] = largest_of(v[j]);
           }
-          split_operand<WD>(v, &hi, &lo);
+        }
+        if constexpr (kScaled) {
+          int e[kA];
+          bool some = scaled;
+#pragma unroll
+          for (int j = 0; j < kA; ++j) {  // eight lanes have the row's values
+            most[j] = lane_max<0xB1>(most[j]);
+            most[j] = lane_max<0x4E>(most[j]);
+            most[j] = lane_max<0x141>(most[j]);
+            e[j] = split_exponent(most[j]);
+            some = some || e[j] != 0;
+          }
+          if (some) {
+#pragma unroll
+            for (int j = 0; j < kA; ++j) {
+              const int u = tid + j * S::kNT, r = u >> 3;
+              // Rows whose values were large once stay at the exponent that
+              // these took or 0: their accumulators times 2^40 might overflow.
+              const int32_t was = row_exp[r];
+              if (row_pos[r] < 0 || ((was & 1) && e[j] > 0)) e[j] = 0;
+              scale_values(v[j], e[j]);
+              if ((u & 7) == 0) {
+                row_step[r] = e[j] - (was >> 1);
+                row_exp[r] = 2 * e[j] | (was & 1) | (e[j] < 0);
+                if (e[j] != 0) any_scaled = 1;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+          const int u = tid + j * S::kNT, r = u >> 3, c = u & 7;
+          u32x4 hi, lo;
+          split_operand<WD>(v[j], &hi, &lo);
           const int to = (r % HM) * 64 + ((c ^ (r & 7)) * 8);
           *reinterpret_cast<u32x4*>((r < HM ? a00 : a01) + to) = hi;
           *reinterpret_cast<u32x4*>((r < HM ? a10 : a11) + to) = lo;
         }
         store_lora_b(b00, b01);
         __syncthreads();
+        if constexpr (kScaled) {
+          scaled = uniform(any_scaled) != 0;
+          if (scaled) rescale([&](int r) { return row_step[r]; });
+        }
         bool odd = false;
         for (int i = 0; i < adapters; i += side, odd = !odd) {
           if (i + side < adapters) load_lora_b(i + side);
@@ -426,6 +516,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
         }
       }
     }
+    if (scaled) rescale([&](int r) { return -(row_exp[r] >> 1); });
     odd_values = adapters > 0 && uniform(odd_found) != 0;
     if (odd_values) {  // the A buffers, free now, take a code for every result
 #pragma unroll 1

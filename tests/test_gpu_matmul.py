@@ -438,3 +438,66 @@ def test_lora_linear_odd_projections_stay_in_their_window(T, K, dtype):
     odd = check_against_ieee(o, x, w, slices, start, lens, idx)
     rows = list(range(start[1], start[2])) + list(range(start[3], T))
     assert odd[rows, :40].all() and int(odd.sum()) == 40 * len(rows)
+
+
+def scaled_bound(x, w, slices, start, lens, idx, scale, left):
+    """(exact result, error bound) of a float32 result whose values v = scale A x each keep an error of
+    `left` of the largest one of their row and slice, whatever its size (down to 2^-65 itself)."""
+    x, w = x.double().cpu(), w.double().cpu()
+    e = U.sum_error(x.shape[1])
+    y, mag = x @ w.t(), x.abs() @ w.abs().t()
+    err = e * mag
+    for st, n, a in zip(start, lens, idx):
+        for la, lb, off in slices if a >= 0 else ():
+            A, B, r, c = la[a].double().cpu(), lb[a].double().cpu(), slice(st, st + n), slice(off, off + lb.shape[1])
+            v = scale * (x[r] @ A.t())
+            ev = scale * e * (x[r].abs() @ A.abs().t()) + left * v.abs().amax(dim=1, keepdim=True) + 2.0 ** -65
+            y[r, c] += v @ B.t()
+            m = (v.abs() + ev) @ B.abs().t()
+            mag[r, c] += m
+            err[r, c] += ev @ B.abs().t() + U.sum_error(2 * A.shape[0]) * m
+    err = err + 4 * 2.0 ** -23 * mag
+    return y, U.rounded(y, err, F32)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** -20, 2.0 ** -12, 2.0 ** -4, 2.0 ** 9, 2.0 ** 17, 2.0 ** 40])
+@pytest.mark.parametrize("T,K", ODD_SHAPES)
+def test_lora_linear_float16_keeps_projections_of_any_size(T, K, scale):
+    """float16 weights, float32 results, nothing but the adapters: the values v lie far below and far
+    above float16's own range and keep 22 bits."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T + K)
+    H, N, L = 72, 4096 if T > 1000 else 152, 3
+    x, w = normal(gen, T, H, dtype=F16), torch.zeros(N, H, dtype=F16, device="cuda")
+    slices = [(normal(gen, L, K, H, sigma=H ** -0.5, dtype=F16), normal(gen, L, N, K, dtype=F16), 0)]
+    start, lens, idx = [0, T // 3], [T // 3, T - T // 3], [0, 1]
+    o = torch.zeros(T, N, dtype=F32, device="cuda")
+    sg.sgmv_lora_linear(x, w, slices, o, i64(start), i64(lens), i64(idx), 2, T, scaling=scale)
+    want, bound = scaled_bound(x, w, slices, start, lens, idx, scale, 2.0 ** -22)
+    U.assert_within(o, want, bound)
+
+
+@pytest.mark.parametrize("T,K", ODD_SHAPES)
+def test_lora_linear_float16_projections_of_unlike_sizes(T, K):
+    """Slices, adapters and parts of the rank whose values differ by powers of two, beside a shared
+    projection that has to stay as it is, in rows without an adapter too."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T + K)
+    H, L = 72, 4
+    widths, offs, N = [40, 24, 32], [0, 40, 80], 4096 if T > 1000 else 152
+    x, w = normal(gen, T, H, dtype=F16), normal(gen, N, H, sigma=H ** -0.5, dtype=F16)
+    slices = [(normal(gen, L, K, H, sigma=H ** -0.5, dtype=F16), normal(gen, L, n, K, dtype=F16), off)
+              for n, off in zip(widths, offs)]
+    for s, p in enumerate((2.0 ** 10, 2.0 ** -8, 1.0)):
+        slices[s][0].mul_(p)
+    for a in range(L):
+        slices[a % 3][0][a].mul_(2.0 ** -(2 * a))
+    slices[2][0][:, K // 2:].mul_(2.0 ** -6)
+    cut = sorted(np.random.default_rng(T).integers(0, T + 1, 4).tolist())
+    start, lens = [0] + cut, [b - a for a, b in zip([0] + cut, cut + [T])]
+    idx = [2, 0, -1, 3, 1]
+    for scale in (2.0 ** 11, 2.0 ** -9):
+        o = torch.zeros(T, N, dtype=F32, device="cuda")
+        sg.sgmv_lora_linear(x, w, slices, o, i64(start), i64(lens), i64(idx), 5, T, scaling=scale)
+        want, bound = scaled_bound(x, w, slices, start, lens, idx, scale, 2.0 ** -22)
+        U.assert_within(o, want, bound)
