@@ -361,9 +361,9 @@ sgmv_status sgmv_fused_shrink_expand(sgmv_matrix inputs, const sgmv_fused_slice*
  * shared projection: also rows of index -1 segments (requests without an
  * adapter), rows outside every segment, and all rows when num_slices or
  * batches is 0.  Sums in fp32, one rounding (nearest even) to the output
- * dtype; v_s is kept in fp32 and enters the second product as two 16-bit
- * parts, so it is not rounded to the weights' dtype: bfloat16 parts hold 16
- * bits of every value, float16 parts (scaled by a power of two where the
+ * dtype; v_s is kept in fp32 and enters the second product as 16-bit parts, so
+ * it is not rounded to the weights' dtype: bfloat16 parts hold 16 bits of
+ * every value (all 24 where out is fp32), float16 parts (scaled by a power of two where the
  * values lie outside 2^-2 .. 2^15) 22 bits of the largest of a row's values
  * in the slice, down to 2^-65.  Values and weights that are not finite
  * multiply as in IEEE arithmetic and reach their own rows and windows alone.

@@ -230,23 +230,47 @@ __device__ __forceinline__ AdapterDesc adapter_desc(int i) {
   return AdapterDesc{d.b, d.v, d.n, d.offset};
 }
 
-// Eight finite float32 values as two packed operands of the 16-bit weight
-// dtype, v = hi + lo to 16 (bfloat16) or 22 (float16) bits: one rounding to the
-// weights' dtype would leave the adapters' share of a float32 result with an
-// error of 2^-9 or 2^-12.  float16 has these bits from 2^-2 to 2^15 only (lo
-// ends at 2^-24, hi at 65504): see split_exponent.
+// Eight finite float32 values as packed operands of the 16-bit weight dtype:
+// one rounding to the weights' dtype would leave the adapters' share of a
+// float32 result with an error of 2^-9 or 2^-12.  v = hi + lo to 16 (bfloat16)
+// or 22 (float16) bits; what bfloat16 leaves, third_operand, makes it exact
+// and is multiplied where results are float32 (half as many matrix
+// instructions again, invisible after a rounding to 16 bits).  float16 has its
+// bits from 2^-2 to 2^15 only (lo ends at 2^-24, hi at 65504): see
+// split_exponent.  Values that would round up to an infinity of bfloat16 leave
+// more to the lower parts instead; the parts are added from the lowest on, so
+// that hi + lo, which may round up too, is no step of an exact sum.
+constexpr float kLargestBf16 = 3.38953139e38f;  // 2^128 - 2^120
+template <int WD>
+__device__ __forceinline__ uint32_t high_pair(float v0, float v1) {
+  if constexpr (WD == BF16) {
+    v0 = __builtin_amdgcn_fmed3f(v0, -kLargestBf16, kLargestBf16);
+    v1 = __builtin_amdgcn_fmed3f(v1, -kLargestBf16, kLargestBf16);
+  }
+  return pack2<WD>(v0, v1);
+}
+
 template <int WD>
 __device__ __forceinline__ void split_operand(const float* v, u32x4* hi, u32x4* lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t h = pack2<WD>(v[2 * i], v[2 * i + 1]);
-    const float h0 = widen<WD>(h & 0xFFFFu), h1 = widen<WD>(h >> 16);
-    // the rest of an infinity is nothing (inf - inf would be NaN)
-    const float r0 = __builtin_isinf(h0) ? 0.f : v[2 * i] - h0;
-    const float r1 = __builtin_isinf(h1) ? 0.f : v[2 * i + 1] - h1;
+    const uint32_t h = high_pair<WD>(v[2 * i], v[2 * i + 1]);
     (*hi)[i] = h;
-    (*lo)[i] = pack2<WD>(r0, r1);
+    (*lo)[i] = pack2<WD>(v[2 * i] - widen<WD>(h & 0xFFFFu), v[2 * i + 1] - widen<WD>(h >> 16));
   }
+}
+
+// What hi + lo leave of eight values, at most seven bits each: exact.
+__device__ __forceinline__ u32x4 third_operand(const float* v) {
+  u32x4 third;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = high_pair<BF16>(v[2 * i], v[2 * i + 1]);
+    const float r0 = v[2 * i] - widen<BF16>(h & 0xFFFFu), r1 = v[2 * i + 1] - widen<BF16>(h >> 16);
+    const uint32_t l = pack2<BF16>(r0, r1);
+    third[i] = pack2<BF16>(r0 - widen<BF16>(l & 0xFFFFu), r1 - widen<BF16>(l >> 16));
+  }
+  return third;
 }
 
 // float16: the e for which a row's values times 2^e have 22 bits of the largest

@@ -104,8 +104,10 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
               odd_found = 1;
               bv = drop_odd<WD>(bv);
             }
-            f32x4 d = mfma<WD>(bv, hi, WD == F16 ? f32x4{} : sum[f]);
+            f32x4 d = WD == F16 ? f32x4{} : sum[f];
+            if (WD == BF16 && p.out_dtype == F32) d = mfma<WD>(bv, third_operand(v), d);
             d = mfma<WD>(bv, lo, d);
+            d = mfma<WD>(bv, hi, d);
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[f][j] = WD == F16 ? sum[f][j] + ldexpf(d[j], -e) : d[j];
           }

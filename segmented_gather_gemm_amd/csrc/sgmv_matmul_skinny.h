@@ -134,6 +134,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
       for (int k = 0; k < p.K; k += 32) {
         const int at = k + lq * 8;
         u32x4 raw[MB][2], hi[MB], lo[MB];
+        [[maybe_unused]] u32x4 third[MB];  // bfloat16 with float32 results
+        const bool exact = WD == BF16 && p.out_dtype == F32;
         [[maybe_unused]] int e[MB];  // float16: exponent of a token's values in the parts
 #pragma unroll
         for (int m = 0; m < MB; ++m)
@@ -184,6 +186,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
                 scale_values(v, e[m]);
               }
               split_operand<WD>(v, &hi[m], &lo[m]);
+              if (exact) third[m] = third_operand(v);
             }
           }
 #pragma unroll
@@ -195,8 +198,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
               if (__ballot(own) == 0) continue;
 #pragma unroll
               for (int n = 0; n < NB; ++n) {
-                f32x4 d = mfma<WD>(bv[j][n], hi[m], f32x4{});
+                f32x4 d{};
+                if (exact) d = mfma<WD>(bv[j][n], third[m], d);
                 d = mfma<WD>(bv[j][n], lo[m], d);
+                d = mfma<WD>(bv[j][n], hi[m], d);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   const float y = WD == F16 ? ldexpf(d[q], -e[m]) : d[q];

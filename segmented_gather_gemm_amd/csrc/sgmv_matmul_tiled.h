@@ -341,6 +341,9 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     constexpr int kA = S::BM * 8 / S::kNT, kB = S::BN * 8 / S::kNT;  // blocks per thread
     // Width of an adapter in a step, log2 of 8 elements, and adapters a step.
     const int wide = p.K <= 8 ? 0 : p.K <= 16 ? 1 : p.K <= 32 ? 2 : 3, side = 8 >> wide;
+    // bfloat16 with float32 results: a third part, in the place of the second B
+    // buffer (one more barrier an adapter).
+    const bool exact = WD == BF16 && p.out_dtype == F32;
     int mine[2 * FM];
 #pragma unroll
     for (int m = 0; m < 2 * FM; ++m)
@@ -472,6 +475,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
           u32x4 hi, lo;
           split_operand<WD>(v[j], &hi, &lo);
           const int to = (r % HM) * 64 + ((c ^ (r & 7)) * 8);
+          if (exact) *reinterpret_cast<u32x4*>((r < HM ? b10 : b11) + to) = third_operand(v[j]);
           *reinterpret_cast<u32x4*>((r < HM ? a00 : a01) + to) = hi;
           *reinterpret_cast<u32x4*>((r < HM ? a10 : a11) + to) = lo;
         }
@@ -482,7 +486,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
           if (scaled) rescale([&](int r) { return row_step[r]; });
         }
         bool odd = false;
-        for (int i = 0; i < adapters; i += side, odd = !odd) {
+        for (int i = 0; i < adapters; i += side, odd = !odd && !exact) {
           if (i + side < adapters) load_lora_b(i + side);
           const uint16_t* B0 = odd ? b10 : b00;
           const uint16_t* B1 = odd ? b11 : b01;
@@ -496,8 +500,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
             for (int m = 0; m < 2 * FM; ++m) {
               if (__ballot(mine[m] == slot) == 0) continue;  // none of these 16 rows
 #pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                const uint16_t* A = m < FM ? (part ? a10 : a00) : (part ? a11 : a01);
+              for (int part = 2; part >= 0; --part) {
+                if (part == 2 && !exact) continue;
+                const uint16_t* A = m < FM ? (part == 0 ? a00 : part == 1 ? a10 : b10)
+                                           : (part == 0 ? a01 : part == 1 ? a11 : b11);
                 u32x4 x = operand_of(A, wm * FM + m % FM, s, erow, eq);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = mine[m] == slot ? x[j] : 0u;
@@ -509,7 +515,8 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
             }
           }
           if (i + side < adapters) {
-            if (odd) store_lora_b(b00, b01);
+            if (exact) __syncthreads();  // every wave has read the weights there
+            if (odd || exact) store_lora_b(b00, b01);
             else store_lora_b(b10, b11);
           }
           __syncthreads();

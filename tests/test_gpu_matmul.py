@@ -501,3 +501,32 @@ def test_lora_linear_float16_projections_of_unlike_sizes(T, K):
         sg.sgmv_lora_linear(x, w, slices, o, i64(start), i64(lens), i64(idx), 5, T, scaling=scale)
         want, bound = scaled_bound(x, w, slices, start, lens, idx, scale, 2.0 ** -22)
         U.assert_within(o, want, bound)
+
+
+@pytest.mark.parametrize("dtype,scale", [(BF16, 1.0), (BF16, 2.0 ** -60), (BF16, 2.0 ** 127), (F16, 1.0), (F16, 2.0 ** -30), (F16, 2.0 ** 40)])
+@pytest.mark.parametrize("T,K", ODD_SHAPES)
+def test_lora_linear_float32_results_hold_all_bits_of_the_projections(T, K, dtype, scale):
+    """lora_B picks one value v a column, so that a float32 result is v itself: 24 bits of it with
+    bfloat16 weights (values up to float32's largest), 22 with float16 weights."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T + K)
+    H, N, L = 72, 4096 if T > 1000 else 152, 3
+    bits, parts = (8, 3) if dtype == BF16 else (11, 2)
+    x = torch.zeros(T, H, dtype=dtype)
+    la = torch.zeros(L, K, H, dtype=dtype)
+    for i, h in enumerate((3, 40, 71)[:parts]):
+        x[:, h] = 2.0 ** (-bits * i)
+        la[:, :, h] = (torch.randint(2 ** (bits - 1), 2 ** bits, (L, K), generator=gen) * 2.0 ** (1 - bits)).to(dtype)
+    la[1, :, 3] = 2 - 2.0 ** (1 - bits)  # the largest: rounding it to the parts' type goes up to 2
+    sign = torch.where(torch.rand(T, generator=gen) < 0.5, -1.0, 1.0)
+    x = (x * sign[:, None]).to(dtype).cuda()
+    lb = torch.zeros(L, N, K, dtype=dtype)
+    lb[:, torch.arange(N), torch.arange(N) % K] = 1.0
+    w = torch.zeros(N, H, dtype=dtype, device="cuda")
+    o = torch.full((T, N), 7.0, dtype=F32, device="cuda")
+    start, lens, idx = [0, T // 3], [T // 3, T - T // 3], [0, 1]
+    sg.sgmv_lora_linear(x, w, [(la.cuda(), lb.cuda(), 0)], o, i64(start), i64(lens), i64(idx), 2, T, scaling=scale)
+    for st, n, a in zip(start, lens, idx):
+        v = scale * (x[st:st + n].double().cpu() @ la[a].double().t())
+        assert torch.equal(v, v.float().double())
+        assert torch.equal(o[st:st + n].double().cpu(), v[:, torch.arange(N) % K])
