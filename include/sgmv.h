@@ -393,7 +393,8 @@ sgmv_status sgmv_fused_shrink_expand(sgmv_matrix inputs, const sgmv_fused_slice*
  *               own; it must not overlap any other argument.
  *
  * Returns SGMV_OK, or a status with nothing launched; total_tokens == 0 or
- * out.cols == 0 return SGMV_OK without a launch.
+ * out.cols == 0 return SGMV_OK without a launch; SGMV_ERR_UNSUPPORTED for
+ * problems of more threads than a launch holds (from 2^36 results on).
  */
 sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void* bias,
                              const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
@@ -436,7 +437,8 @@ sgmv_status sgmv_lora_linear_workspace_bytes(int64_t tokens, int num_slices, int
  *               sgmv_route writes them for a batch of routed tokens.
  *
  * Returns SGMV_OK, or a status with nothing launched; batches == 0, no
- * expert, no row or no column return SGMV_OK without a launch.
+ * expert, no row or no column return SGMV_OK without a launch;
+ * SGMV_ERR_UNSUPPORTED as for sgmv_lora_linear.
  */
 sgmv_status sgmv_grouped_gemm(sgmv_matrix inputs, sgmv_stack weights, sgmv_matrix out,
                               const int64_t* row_indices, const int64_t* b_seq_start_loc,

@@ -119,8 +119,11 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
   // Grouped: at most ceil(T / rows) + min(batches, T) row tiles.
   plan->row_tiles = tiles(p.T, plan->rows) + (p.grouped ? (p.batches < p.T ? p.batches : p.T) : 0);
   plan->col_tiles = tiles(p.N, plan->cols);
-  if (plan->row_tiles * plan->col_tiles > INT32_MAX)
-    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^31-1 work units");
+  // A launch holds fewer than 2^32 threads: refused here, ahead of the adapters'
+  // own launch (64 x 64 tiles reach it at 2^36 results).
+  if (plan->row_tiles * plan->col_tiles > (int64_t)UINT32_MAX / plan->threads)
+    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^32-1 threads (%lld tiles of %d x %d)",
+                (long long)(plan->row_tiles * plan->col_tiles), plan->rows, plan->cols);
   return SGMV_OK;
 }
 

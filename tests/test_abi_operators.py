@@ -214,3 +214,15 @@ def test_python_wrappers_reject_host_tensors():
         sg.sgmv_route(x, x, i, i, i, i, i)
     with pytest.raises(ValueError, match="GPU"):
         sg.sgmv_combine(x, x, i, x)
+
+
+@pytest.mark.parametrize("rows,status", [(1 << 30, UNSUPPORTED), ((1 << 30) + 5, UNSUPPORTED)])
+def test_products_of_more_threads_than_a_launch_holds(rows, status):
+    """2^36 results and more in 64 x 64 tiles of 256 threads (hidden 65: no other kernel takes it) are
+    refused before the adapters' projection is launched."""
+    st, msg = lora(x=Matrix(FAKE, BF16, rows, 65, 65), w=Matrix(FAKE, BF16, 64, 65, 65), out=Matrix(FAKE, BF16, rows, 64, 64),
+                   slices=[slice_(H=65)], ws_bytes=1 << 62)
+    assert st == status and "threads" in msg
+    st = sg.lib.sgmv_grouped_gemm(Matrix(FAKE, BF16, rows, 65, 65), Stack(FAKE, BF16, 2, 64, 65), Matrix(FAKE, BF16, rows, 64, 64),
+                                  None, FAKE, FAKE, None, 2, 5, 0, None)
+    assert st == status and "threads" in error()
