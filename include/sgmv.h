@@ -382,7 +382,8 @@ sgmv_status sgmv_fused_shrink_expand(sgmv_matrix inputs, const sgmv_fused_slice*
  * b_seq_start_loc, seq_lens, lora_indices, batches, max_seq_len, stream:
  *               as for sgmv_expand_slice, with the same device-side
  *               preconditions (a segment that breaks one gets the shared
- *               projection alone).
+ *               projection alone; where segments overlap, any row of a
+ *               segment may hold unspecified values).
  * scale         fp32 factor of the adapters' part.
  * add_inputs    nonzero: accumulate onto out; zero: overwrite.
  * workspace, workspace_bytes:
@@ -433,7 +434,9 @@ sgmv_status sgmv_lora_linear_workspace_bytes(int64_t tokens, int num_slices, int
  *               outside [0, input_rows) is the product of a row of zeros.
  * expert_indices  device int64[batches] or NULL.
  * b_seq_start_loc, seq_lens, batches, max_seq_len, stream: as for
- *               sgmv_expand_slice, with the same device-side preconditions.
+ *               sgmv_expand_slice, with the same device-side preconditions;
+ *               where segments overlap, any row of a segment may hold
+ *               unspecified values (rows outside all stay untouched).
  *               sgmv_route writes them for a batch of routed tokens.
  *
  * Returns SGMV_OK, or a status with nothing launched; batches == 0, no

@@ -73,7 +73,8 @@ __device__ __forceinline__ int32_t read_group(const MatmulParams& p, int32_t b, 
 // NT / 64 + 4 words of LDS).  Grouped: every workgroup counts the segments'
 // tiles (a block scan over contiguous runs of segments, so the order of
 // tiles is the order of segments), and the thread whose run holds the tile
-// looks it up.
+// looks it up.  None may have it where segments overlap, a broken
+// precondition, and their tiles' sum passes 32 bits.
 template <int NT>
 __device__ __forceinline__ TileLoc find_tile(const MatmulParams& p, int32_t tile_rows,
                                              int32_t* sh) {
@@ -94,6 +95,7 @@ __device__ __forceinline__ TileLoc find_tile(const MatmulParams& p, int32_t tile
   for (int32_t b = b0; b < b1; ++b) mine += read_group(p, b, tile_rows, &row, &end, &e);
   const int32_t incl = wave_inclusive_sum(mine);
   if (lane == 63) sh[wave] = incl;
+  if (tid == 0) sh[NT / 64] = -1;  // no tile, should none of the threads below have it
   __syncthreads();
   int32_t before = 0, total = 0;
 #pragma unroll

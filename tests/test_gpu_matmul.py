@@ -530,3 +530,20 @@ def test_lora_linear_float32_results_hold_all_bits_of_the_projections(T, K, dtyp
         v = scale * (x[st:st + n].double().cpu() @ la[a].double().t())
         assert torch.equal(v, v.float().double())
         assert torch.equal(o[st:st + n].double().cpu(), v[:, torch.arange(N) % K])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,H", [(60, 64), (700, 64), (700, 67)])
+def test_grouped_overlapping_segments_stay_in_their_rows(T, H, gated):
+    """Overlapping segments break a precondition and their values are unspecified; rows outside all of
+    them stay as they are."""
+    import segmented_gather_gemm_amd as sg
+    gen = torch.Generator().manual_seed(T)
+    N, B = 96, 500
+    x, w = normal(gen, T, H), normal(gen, 3, 2 * N if gated else N, H)
+    full, o = guarded(T, N, BF16, 5, gen)
+    o0 = o.clone()
+    start, lens = [T // 4] * B, [T // 2] * B
+    sg.sgmv_grouped_gemm(x, w, o, i64(start), i64(lens), i64([b % 3 for b in range(B)]), B, T, gated=gated)
+    outside = list(range(T // 4)) + list(range(T // 4 + T // 2, T))
+    assert torch.equal(o[outside], o0[outside]) and bool((full[:, N:] == 7.0).all())
