@@ -67,12 +67,13 @@ bool tiled_fits(const sgmv::MatmulParams& p) {
 // whichever ends first, by the rounds of workgroups that each takes.  A round
 // of large tiles is taken as 100; of medium ones as 34 with one workgroup per
 // compute unit, 57 with two, and 75 past two rounds, where their twice as
-// many bytes per product bind (measured: dense, hidden 4096, 4096 columns,
-// 4096 rows 98 us on 256 large tiles and 115 us on 1024 medium ones, 2048 rows
-// 79 and 60 us, 512 rows 72 and 32 us; grouped, 8 experts x 1024 rows, hidden
-// 14336, 885 and 1130 us, 64 experts x 32 rows 164 and 151 us; where they are
-// near each other, 32 experts x 188 rows 115 and 119 us, it may miss by 5%).  A
-// segment fills half of its last tile on average.
+// many bytes per product bind.  Measured, large and medium, bfloat16, weights
+// from memory: dense, hidden 4096, 4096 columns, 4096 rows 99 and 132 us (256
+// large tiles, 1024 medium ones), 2048 rows 81 and 70, 512 rows 79 and 46;
+// grouped, 8 experts x 1024 rows, hidden 14336, 4096 columns 703 and 1031 us,
+// 64 experts x 32 rows, hidden 2048, 2 x 1408 columns 180 and 167.  Where they
+// are near each other (32 experts x 188 rows of the same, 124 and 121 us) it
+// may miss by 5%.  A segment fills half of its last tile on average.
 sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int cus) {
   const sgmv::TiledKernel l = sgmv::matmul_tiled_large(wd, mode);
   const sgmv::TiledKernel m = sgmv::matmul_tiled_medium(wd, mode);
@@ -97,20 +98,29 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
     // The kernel for few rows where there would be few tiles: dense calls of
     // up to 32 rows (64 with adapters, whose share its waves divide), and
     // segments of up to 16 rows whose 128 x 128 tiles leave half of the compute
-    // units idle (hidden 4096, 4096 columns: 17 rows 11.4 us against 26.5 in
-    // medium tiles; 64 rows without adapters are even, 25.4 and 27.1, and with
-    // 14336 columns the tiles win, 49.0 and 28.5 us; with 32 adapters the
-    // waves' 50 us beat the tiles' 83; 8 experts x 4 rows 20.9 and 18.2 us).
+    // units idle.  It reads the rows again for every 16 or 32 columns, which
+    // costs more than 128 x 128 tiles do once it has many workgroups of more
+    // than 16 rows.  Measured, few-row kernel and 128 x 128 tiles, bfloat16,
+    // hidden 4096, weights from memory, us.  Dense: 1 row, 4096 and 28672 columns
+    // 10 and 37, 41 and 52; 16 rows 12 and 38, 60 and 53; 32 rows, 4096, 10240
+    // and 14336 columns 15 and 38, 38 and 40, 50 and 42.  Rank 16, 32 adapters:
+    // 32 rows, 6144, 14336 and 28672 columns 43 and 69, 73 and 73, 127 and 85;
+    // 64 rows 50 and 74, 91 and 78, 170 and 90 (4 adapters 45 and 59, 80 and
+    // 64, 150 and 76; 64 adapters of rank 64, 14336 columns 129 and 192).
+    // Segments of 4 rows: 4 experts, hidden 2048, 2 x 1408 columns 17 and 23, 2
+    // experts, hidden 14336, 4096 columns 49 and 125; past half of the units
+    // 13 experts, 2 x 1408 columns 36 and 45, but hidden 1408, 2048 columns 24
+    // and 19, 32 experts x 8 rows 54 and 36.
     const TiledKernel m = matmul_tiled_medium(wd, mode);
-    const int64_t few = 32 * (p.num_slices > 0 ? 2 : 1);
+    const bool adapted = p.num_slices > 0;
+    const TiledKernel f = p.grouped || p.T <= 16 ? matmul_skinny_16(wd, mode)
+                          : p.T <= 32           ? matmul_skinny_32(wd, adapted)
+                                                : matmul_skinny_64_adapted(wd);
     const int64_t used = p.batches < p.T ? p.batches : p.T;
-    const bool skinny = p.grouped ? tiles(p.T, p.batches) <= 16 &&
-                                        2 * used * tiles(p.N, m.cols) <= cus
-                                  : p.T <= few;
-    const TiledKernel k = !skinny                   ? pick_tiled(p, wd, mode, cus)
-                          : p.grouped || p.T <= 16 ? matmul_skinny_16(wd, mode)
-                          : p.T <= 32              ? matmul_skinny_32(wd, p.num_slices > 0)
-                                                   : matmul_skinny_64_adapted(wd);
+    const bool few = p.grouped ? tiles(p.T, p.batches) <= 16 && 2 * used * tiles(p.N, m.cols) <= cus
+                               : p.T <= 16 || (p.T <= (adapted ? 64 : 32) &&
+                                               f.rows * tiles(p.N, f.cols) <= (adapted ? 160 : 80) * (int64_t)cus);
+    const TiledKernel k = few ? f : pick_tiled(p, wd, mode, cus);
     *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0};
   } else {
     *plan = Plan{matmul_generic_kernel(wd, gated), kGenericRows, kGenericCols, kThreads, 0, 0};
