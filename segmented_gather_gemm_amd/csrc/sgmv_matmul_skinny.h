@@ -12,13 +12,17 @@
 // contraction inside the workgroup gives a 4096-wide projection 256
 // workgroups of 16 columns, with no partial sums in memory.
 //
-// Measured: one row, 4096 x 4096 weights 7.9 us (4.2 TB/s; the launch and the
-// first loads' latency are about half of it), with its adapter 9.0 us; 17 rows
-// 11.4 us; 64 rows with adapters through 6144 columns 41 us, where the operands
-// of 64 rows through one compute unit's L1 bind (768 KiB a workgroup).  Two
-// steps ahead beat four and eight (16 experts' gated products 30 against 35
-// and 55 us: fewer registers, more workgroups on a compute unit); 16 columns
-// beat 32 for up to 32 rows, 32 beat 16 for 64 (25.5 against 39.7 us).
+// Measured (bfloat16, hidden 4096, weights from memory, us a call): one row, 4096
+// columns 9.9 (3.4 TB/s; the launch and the first loads' latency are about half
+// of it), 14336 columns 25.5 (4.6 TB/s); 17 rows, 4096 columns 12.4; 64 rows with
+// 32 adapters through 6144 columns 49.8, 40 of them this kernel's, where the
+// operands of 64 rows through one compute unit's L1 bind (768 KiB a
+// workgroup).  Two steps ahead, against one and four: 10.0, 10.1 and 9.7 for
+// one row, 17.8, 18.6 and 17.5 with its adapter, 15.2, 14.1 and 16.7 for 32 rows,
+// 17.0, 16.2 and 17.6 for 4 gated experts of 4 rows (hidden 2048, 2 x 1408).  16
+// columns a workgroup against 32: 10.0 and 12.8 for one row, 15.2 and 20.1 for
+// 32; 64 rows with 32 adapters take 32 columns, 49.8 and 75.6 (with 4 adapters
+// and 4096 columns 44.4 and 39.1).
 #pragma once
 
 #include "sgmv_matmul.h"

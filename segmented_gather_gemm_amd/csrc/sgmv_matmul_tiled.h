@@ -19,19 +19,20 @@
 // instructions come in two parts of 32 along the contraction.  During part 1
 // all operands of the next step are read into registers (three sets of a
 // part's operands, rotating), so that its LDS is free half a step later and is
-// refilled with the step after next, most of it during part 0; the loads have
+// refilled with the step after next, most or all of it during part 0; the loads have
 // one to one and a half steps to arrive.  Evenly spread they cost least: all
 // of them in the first half of part 0 is 6-8% slower.  Barriers: before part 1 (the next step has
 // arrived, for every wave) and before part 0 (every wave has read it).
 //
-// What bounds it: with 256 x 256 tiles the matrix instructions (busy 77% of the
-// compute units' time at 8192 x 8192 x 8192, 740 us, 1490 TFLOP/s; the rest is
-// barriers and the tiles' first and last steps); before loads had more
+// What bounds it: with 256 x 256 tiles the matrix instructions (busy 79% of the
+// compute units' time at 8192 x 8192 x 8192, 732-742 us, 1480-1501 TFLOP/s; the rest
+// is barriers and the tiles' first and last steps); before loads had more
 // than one step to arrive, the loads did (884 us).  Prefill of 16384 tokens,
-// hidden 4096 -> 28672: 2696 us = 1427 TFLOP/s, with 64 adapters of rank 64
-// 3050-3120 us.  The 128 x 128 tile moves twice the bytes per product and wins
-// where the large one leaves compute units idle (512 x 4096 x 4096: 32 us
-// against 72) and for experts with few rows, which it reads at 3.5 TB/s.
+// hidden 4096 -> 28672: 2662-2694 us = 1428-1446 TFLOP/s, with 64 adapters of
+// rank 64 3002 us (segments of whole tiles; 3118-3174 of uneven lengths).  The 128 x
+// 128 tile moves twice the bytes per product and wins where the large one
+// leaves compute units idle (512 x 4096 x 4096: 41 us against 79) and for
+// experts with few rows (64 of 96 rows: their weights at 4.6 TB/s).
 #pragma once
 
 #include <type_traits>
