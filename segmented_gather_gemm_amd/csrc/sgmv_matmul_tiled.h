@@ -219,12 +219,15 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   };
   constexpr int kReads = 2 * (FM + FN), kLoads = 4 * LL;
   // Loads of a step that part 0 issues, of 16 in large tiles and of 8 in small
-  // ones: 10, 12 and all of 16 take 2697, 2695 and 2814 us at 16384 x 28672 x
+  // ones.  10, 12 and all of 16 take 2697, 2695 and 2814 us at 16384 x 28672 x
   // 4096, 3002, 3014 and 3110 us with 64 adapters of rank 64 beside it, 742, 747
-  // and 755 us at 8192 x 8192 x 8192; 5, 6 and all of 8 take 47, 45 and 42 us at
-  // 512 x 4096 x 4096, 60, 58 and 55 us with adapters, 170, 168 and 159 us for
-  // 64 experts of 96 rows (hidden 2048, 2 x 1408 columns).
-  constexpr int kEarly = S::kOccupancy == 1 ? kLoads * 5 / 8 : kLoads;
+  // and 755 us at 8192 x 8192 x 8192.  6 and all of 8 take 45 and 42 us at 512 x
+  // 4096 x 4096, 58 and 55 us with adapters; for experts it goes both ways (64 of
+  // 96 rows, hidden 2048, 2 x 1408 columns 168 and 159 us; 8 of 102, hidden 2488, 2
+  // x 8040 columns 215 and 219; 13 of one, hidden 1040, 2744 columns 19.7 and 20.4).
+  constexpr int kEarly = S::kOccupancy == 1                    ? kLoads * 5 / 8
+                         : MODE == kDense || MODE == kAdapted ? kLoads
+                                                              : kLoads * 3 / 4;
   // Step t, whose operands are in sets 0 and 1 + t % 2, with its LDS
   // (A0, A1, B0, B1) free and the next step's in (C0, C1, D0, D1).  BOTH:
   // whether the second A half holds any row.
