@@ -296,6 +296,15 @@ __device__ __forceinline__ uint32_t largest_of(const float* v) {
   return most;
 }
 
+// The largest of lanes l, l + 16, l + 32 and l + 48 in all of them: two swaps of
+// rows of 16 and of halves, of a register with its copy.
+__device__ __forceinline__ uint32_t quarters_max(uint32_t v) {
+  auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = r[0] > r[1] ? r[0] : r[1];
+  r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return r[0] > r[1] ? r[0] : r[1];
+}
+
 // Eight values times 2^e.
 __device__ __forceinline__ void scale_values(float* v, int e) {
 #pragma unroll

@@ -85,11 +85,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
           }
           int e = 0;
           if constexpr (WD == F16) {  // a token's 32 values are in four lanes
-            uint32_t most = largest_of(v);
-            uint32_t other = (uint32_t)__shfl_xor((int)most, 16);
-            most = other > most ? other : most;
-            other = (uint32_t)__shfl_xor((int)most, 32);
-            e = split_exponent(other > most ? other : most);
+            e = split_exponent(quarters_max(largest_of(v)));
             scale_values(v, e);
           }
           u32x4 hi, lo;

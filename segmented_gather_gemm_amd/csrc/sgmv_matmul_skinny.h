@@ -160,18 +160,6 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
                             &bv[j][n]);
             }
           }
-          bool odd = false;
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) odd = odd || any_odd<WD>(bv[j][n]);
-          if (__ballot(odd) != 0) {
-            odd_found = 1;
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j)
-#pragma unroll
-              for (int n = 0; n < NB; ++n) bv[j][n] = drop_odd<WD>(bv[j][n]);
-          }
           if (i == wave) {
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
@@ -182,11 +170,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
                 if (pos[m] >= 0) odd_found = 1;  // else no segment's row: anything may be there
               }
               if constexpr (WD == F16) {  // a token's 32 values are in the lanes lr + 16 q
-                uint32_t most = largest_of(v);
-                uint32_t other = (uint32_t)__shfl_xor((int)most, 16);
-                most = other > most ? other : most;
-                other = (uint32_t)__shfl_xor((int)most, 32);
-                e[m] = split_exponent(other > most ? other : most);
+                e[m] = split_exponent(quarters_max(largest_of(v)));
                 scale_values(v, e[m]);
               }
               split_operand<WD>(v, &hi[m], &lo[m]);
@@ -196,19 +180,30 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
 #pragma unroll
           for (int j = 0; j < kAtOnce; ++j) {
             if (i + j * kW >= adapters) continue;
+            bool odd = false;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) odd = odd || any_odd<WD>(bv[j][n]);
+            if (__ballot(odd) != 0) {
+              odd_found = 1;
+#pragma unroll
+              for (int n = 0; n < NB; ++n) bv[j][n] = drop_odd<WD>(bv[j][n]);
+            }
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
               const bool own = pos[m] == i + j * kW;
               if (__ballot(own) == 0) continue;
+              f32x4 d[NB] = {};
+              if (exact) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n) d[n] = mfma<WD>(bv[j][n], third[m], d[n]);
+              }
 #pragma unroll
               for (int n = 0; n < NB; ++n) {
-                f32x4 d{};
-                if (exact) d = mfma<WD>(bv[j][n], third[m], d);
-                d = mfma<WD>(bv[j][n], lo[m], d);
-                d = mfma<WD>(bv[j][n], hi[m], d);
+                d[n] = mfma<WD>(bv[j][n], lo[m], d[n]);
+                d[n] = mfma<WD>(bv[j][n], hi[m], d[n]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                  const float y = WD == F16 ? ldexpf(d[q], -e[m]) : d[q];
+                  const float y = WD == F16 ? ldexpf(d[n][q], -e[m]) : d[n][q];
                   acc[0][m][n][q] += own ? y : 0.f;
                 }
               }
