@@ -24,15 +24,15 @@
 // of them in the first half of part 0 is 6-8% slower.  Barriers: before part 1 (the next step has
 // arrived, for every wave) and before part 0 (every wave has read it).
 //
-// What bounds it: with 256 x 256 tiles the matrix instructions (busy 79% of the
+// What bounds it: with 256 x 256 tiles the matrix instructions (busy 80% of the
 // compute units' time at 8192 x 8192 x 8192, 732-742 us, 1480-1501 TFLOP/s; the rest
 // is barriers and the tiles' first and last steps); before loads had more
 // than one step to arrive, the loads did (884 us).  Prefill of 16384 tokens,
 // hidden 4096 -> 28672: 2662-2694 us = 1428-1446 TFLOP/s, with 64 adapters of
-// rank 64 3002 us (segments of whole tiles; 3118-3174 of uneven lengths).  The 128 x
+// rank 64 3002 us (segments of whole tiles; 3117-3216 of uneven lengths).  The 128 x
 // 128 tile moves twice the bytes per product and wins where the large one
 // leaves compute units idle (512 x 4096 x 4096: 41 us against 79) and for
-// experts with few rows (64 of 96 rows: their weights at 4.6 TB/s).
+// experts with few rows (64 of 96 rows: their weights at 4.4 TB/s).
 #pragma once
 
 #include <type_traits>
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // and 755 us at 8192 x 8192 x 8192.  6 and all of 8 take 45 and 42 us at 512 x
   // 4096 x 4096, 58 and 55 us with adapters; for experts it goes both ways (64 of
   // 96 rows, hidden 2048, 2 x 1408 columns 168 and 159 us; 8 of 102, hidden 2488, 2
-  // x 8040 columns 215 and 219; 13 of one, hidden 1040, 2744 columns 19.7 and 20.4).
+  // x 8040 columns 215 and 219; 14 of one, hidden 1040, 2744 columns 19.7 and 20.4).
   constexpr int kEarly = S::kOccupancy == 1                    ? kLoads * 5 / 8
                          : MODE == kDense || MODE == kAdapted ? kLoads
                                                               : kLoads * 3 / 4;
