@@ -5,7 +5,7 @@
  * Kernel", Description and I/O Contract), and the LoRA-A projection that
  * produces its inputs (sgmv_shrink, below); further down the operators a
  * serving step runs beside them (sgmv_lora_linear, sgmv_grouped_gemm,
- * sgmv_route, sgmv_combine).  The expand: for each segment b of a packed
+ * sgmv_route, sgmv_combine) and microscaled 4-bit weights for them (sgmv_mx_*).  The expand: for each segment b of a packed
  * batch and each token m of that segment, row t = b_seq_start_loc[b] + m of
  * the output gets, in its column window [slice_offset, slice_offset +
  * slice_size),
@@ -36,7 +36,7 @@
 extern "C" {
 #endif
 
-#define SGMV_ABI_VERSION 6
+#define SGMV_ABI_VERSION 7
 #define SGMV_MAX_SLICES 8      /* slices per multi-slice call                       */
 #define SGMV_MAX_RANK 256      /* largest rank the register-tiled kernels take; larger
                                   ranks (any size) run on the generic kernel */
@@ -504,6 +504,129 @@ sgmv_status sgmv_route_workspace_bytes(int64_t tokens, int64_t experts, int64_t 
  */
 sgmv_status sgmv_combine(sgmv_matrix rows, const float* weights, const int64_t* slots,
                          int64_t top_k, sgmv_matrix out, int add_inputs, hipStream_t stream);
+
+/*
+ * Microscaled 4-bit rows.  32 consecutive values of a row are a block with one
+ * scale byte s, which stands for 2^(s - 127) (255: every value of the block is
+ * NaN); a value is a 4-bit code, a sign (bit 3) and one of 0, .5, 1, 1.5, 2, 3,
+ * 4, 6 (bits 0-2) times the scale.  Two codes a byte, the even value in the low
+ * half.  A row takes whole groups of 128 values, 64 bytes of codes and 4 of
+ * scales each: G = ceil(cols / 128) groups; what lies past cols holds codes 0
+ * and scales other than 255.  (For cols a multiple of 128 this is the usual
+ * layout of (rows, cols / 2) codes and (rows, cols / 32) scales.)
+ */
+typedef struct {
+  void* codes;          /* device, 16-byte aligned                                  */
+  void* scales;         /* device, 4-byte aligned                                   */
+  int64_t num;          /* matrices; row r of matrix e is row e * rows + r          */
+  int64_t rows;
+  int64_t cols;         /* values of a row                                          */
+  int64_t code_stride;  /* bytes from row to row, a multiple of 16, >= 64 G         */
+  int64_t scale_stride; /* bytes from row to row, a multiple of 4, >= 4 G           */
+} sgmv_mx_stack;
+
+/*
+ * sgmv_mx_quantize -- rows as microscaled 4-bit values.  A block whose largest
+ * magnitude is m takes the scale 2^(floor(log2 m) - 2), at least 2^-127 (m = 0
+ * too); each value the code nearest to it over the scale, ties to the even
+ * code, magnitudes above 6 the code of 6; the sign is kept, also of zeros.  A
+ * block that holds an infinity or NaN takes the scale 255 and codes 0.  Every
+ * byte of the rows' groups is written, none past them.
+ *
+ * inputs        device (rows, hidden) f16/bf16/f32, row_stride >= hidden; read only.
+ * out           num * rows == inputs.rows, cols == hidden; must not overlap inputs.
+ *
+ * Returns SGMV_OK, or a status with nothing launched; SGMV_ERR_UNSUPPORTED
+ * for more than 2^30 groups of 128 values.
+ */
+sgmv_status sgmv_mx_quantize(sgmv_matrix inputs, sgmv_mx_stack out, hipStream_t stream);
+
+/*
+ * sgmv_mx_dequantize -- microscaled 4-bit rows as the values they stand for:
+ * out[t] = row row_indices[t] of inputs (its num * rows rows), or row t when
+ * row_indices is NULL (then out.rows == num * rows).  A row whose index lies
+ * outside them is zeros.  Values are exact in f32 and bf16, but that magnitudes
+ * past the dtype's largest become infinities, and rounded to nearest even in
+ * f16.
+ *
+ * inputs        read only.
+ * row_indices   device int64[out.rows] or NULL; read only.
+ * out           device (rows, cols) f16/bf16/f32, row_stride >= cols; must not
+ *               overlap any other argument.
+ *
+ * Returns SGMV_OK, or a status with nothing launched; SGMV_ERR_UNSUPPORTED as
+ * for sgmv_mx_quantize.
+ */
+sgmv_status sgmv_mx_dequantize(sgmv_mx_stack inputs, const int64_t* row_indices, sgmv_matrix out,
+                               hipStream_t stream);
+
+/*
+ * sgmv_mx_lora_linear -- sgmv_lora_linear with a microscaled 4-bit weight.
+ * The shared projection multiplies 4-bit values on both sides,
+ *
+ *     out[t][n] = (add_inputs ? out[t][n] : 0) + bias[n]
+ *                 + sum_h q(inputs)[t][h] * weight[n][h]
+ *                 + sum_k v_s[t][k] * lora_b_s[a][n - off_s][k],
+ *
+ * with q(inputs) the values of the inputs' codes as sgmv_mx_quantize makes them
+ * (within the call, in the workspace); the adapters' part reads the inputs as
+ * they are and is that of sgmv_lora_linear in every respect.  Products of
+ * 4-bit values are exact, sums fp32, one rounding (nearest even).  A block of
+ * the inputs that holds an infinity or NaN makes its row's shared projection
+ * NaN, a weight block of scale 255 its column's.
+ *
+ * inputs        device (total_tokens, hidden) f16/bf16; read only.
+ * weight        one matrix (num == 1) of out.cols rows and hidden columns; read only.
+ * bias          device (out.cols) of the inputs' dtype, or NULL.
+ * slices        as for sgmv_lora_linear, of the inputs' dtype.
+ * workspace, workspace_bytes:
+ *               device buffer of at least sgmv_mx_lora_linear_workspace_bytes()
+ *               bytes, 16-byte aligned, any contents, always needed.  Calls
+ *               that may run at the same time need buffers of their own; it
+ *               must not overlap any other argument.
+ * All else      as for sgmv_lora_linear.
+ *
+ * Returns what sgmv_lora_linear returns, and SGMV_ERR_UNSUPPORTED for inputs of
+ * more than 2^30 groups of 128 values.
+ */
+sgmv_status sgmv_mx_lora_linear(sgmv_matrix inputs, sgmv_mx_stack weight, const void* bias,
+                                const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
+                                const int64_t* b_seq_start_loc, const int64_t* seq_lens,
+                                const int64_t* lora_indices, int64_t batches, int64_t max_seq_len,
+                                float scale, int add_inputs, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of the workspace sgmv_mx_lora_linear takes (num_slices and rank 0
+ * without adapters). */
+sgmv_status sgmv_mx_lora_linear_workspace_bytes(int64_t tokens, int64_t hidden, int num_slices,
+                                                int64_t rank, size_t* bytes);
+
+/*
+ * sgmv_mx_grouped_gemm -- sgmv_grouped_gemm with microscaled 4-bit experts:
+ *
+ *     y[n] = sum_h q(inputs)[src(r)][h] * weights[e][n][h]
+ *
+ * with q(inputs) as in sgmv_mx_lora_linear; plain or gated, rows gathered or
+ * not.
+ *
+ * inputs        device (input_rows, hidden) f16/bf16; read only.
+ * weights       out.cols rows a matrix (gated: 2 * out.cols) of hidden columns; read only.
+ * workspace, workspace_bytes:
+ *               device buffer of at least sgmv_mx_grouped_gemm_workspace_bytes()
+ *               bytes, as in sgmv_mx_lora_linear.
+ * All else      as for sgmv_grouped_gemm.
+ *
+ * Returns what sgmv_grouped_gemm returns, and SGMV_ERR_UNSUPPORTED for inputs
+ * of more than 2^30 groups of 128 values.
+ */
+sgmv_status sgmv_mx_grouped_gemm(sgmv_matrix inputs, sgmv_mx_stack weights, sgmv_matrix out,
+                                 const int64_t* row_indices, const int64_t* b_seq_start_loc,
+                                 const int64_t* seq_lens, const int64_t* expert_indices,
+                                 int64_t batches, int64_t max_seq_len, int gated, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of the workspace sgmv_mx_grouped_gemm takes. */
+sgmv_status sgmv_mx_grouped_gemm_workspace_bytes(int64_t input_rows, int64_t hidden, size_t* bytes);
 
 /* Message for the last non-OK status returned on the calling thread ("" if
  * none).  The pointer stays valid until the thread's next libsgmv call. */

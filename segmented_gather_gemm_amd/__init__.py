@@ -17,7 +17,10 @@ per-token and multi-slice forms, and the two steps fused in one launch
 (sgmv_fused_shrink_expand); and the operators a serving step runs beside them:
 a shared projection with the adapters (sgmv_lora_linear), products grouped by
 expert (sgmv_grouped_gemm), the routing that lays out their segments
-(sgmv_route) and the sum of a token's expert rows (sgmv_combine).
+(sgmv_route) and the sum of a token's expert rows (sgmv_combine); and both
+products with microscaled 4-bit weights (sgmv_mx_lora_linear,
+sgmv_mx_grouped_gemm), which sgmv_mx_quantize makes and sgmv_mx_dequantize
+reads back.
 """
 from __future__ import annotations
 
@@ -38,7 +41,10 @@ EXPORTED_SYMBOLS = ("sgmv_expand_slice", "sgmv_expand_multi_slice", "sgmv_bgmv_e
                     "sgmv_shrink_multi_slice_noalloc",
                     "sgmv_fused_shrink_expand", "sgmv_lora_linear",
                     "sgmv_lora_linear_workspace_bytes", "sgmv_grouped_gemm", "sgmv_route",
-                    "sgmv_route_workspace_bytes", "sgmv_combine", "sgmv_last_error",
+                    "sgmv_route_workspace_bytes", "sgmv_combine", "sgmv_mx_quantize",
+                    "sgmv_mx_dequantize", "sgmv_mx_lora_linear",
+                    "sgmv_mx_lora_linear_workspace_bytes", "sgmv_mx_grouped_gemm",
+                    "sgmv_mx_grouped_gemm_workspace_bytes", "sgmv_last_error",
                     "sgmv_abi_version")
 
 
@@ -63,6 +69,12 @@ class ShrinkSliceDesc(ctypes.Structure):
 
 class FusedSliceDesc(ctypes.Structure):
     _fields_ = [("lora_a", Stack), ("lora_b", Stack), ("slice_offset", ctypes.c_int64)]
+
+
+class MxStack(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("code_stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64)]
 
 
 def _hip_runtimes_mapped():
@@ -135,6 +147,22 @@ def _load_library() -> ctypes.CDLL:
     lib.sgmv_route_workspace_bytes.restype = ctypes.c_int
     lib.sgmv_combine.argtypes = [Matrix, p, p, i64, Matrix, ctypes.c_int, p]
     lib.sgmv_combine.restype = ctypes.c_int
+    lib.sgmv_mx_quantize.argtypes = [Matrix, MxStack, p]
+    lib.sgmv_mx_quantize.restype = ctypes.c_int
+    lib.sgmv_mx_dequantize.argtypes = [MxStack, p, Matrix, p]
+    lib.sgmv_mx_dequantize.restype = ctypes.c_int
+    lib.sgmv_mx_lora_linear.argtypes = [Matrix, MxStack, p, ctypes.POINTER(FusedSliceDesc),
+                                        ctypes.c_int, Matrix, p, p, p, i64, i64, ctypes.c_float,
+                                        ctypes.c_int, p, ctypes.c_size_t, p]
+    lib.sgmv_mx_lora_linear.restype = ctypes.c_int
+    lib.sgmv_mx_lora_linear_workspace_bytes.argtypes = [i64, i64, ctypes.c_int, i64,
+                                                        ctypes.POINTER(ctypes.c_size_t)]
+    lib.sgmv_mx_lora_linear_workspace_bytes.restype = ctypes.c_int
+    lib.sgmv_mx_grouped_gemm.argtypes = [Matrix, MxStack, Matrix, p, p, p, p, i64, i64,
+                                         ctypes.c_int, p, ctypes.c_size_t, p]
+    lib.sgmv_mx_grouped_gemm.restype = ctypes.c_int
+    lib.sgmv_mx_grouped_gemm_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+    lib.sgmv_mx_grouped_gemm_workspace_bytes.restype = ctypes.c_int
     lib.sgmv_last_error.argtypes = []
     lib.sgmv_last_error.restype = ctypes.c_char_p
     lib.sgmv_abi_version.argtypes = []
@@ -494,6 +522,25 @@ def _scratch(device, workspace, need: int):
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
+def _bias(bias, cols: int, dtype, device):
+    if bias is None:
+        return None
+    if bias.device != device or bias.dim() != 1 or bias.shape[0] != cols or \
+            bias.dtype != dtype or not bias.is_contiguous():
+        raise ValueError(f"bias must be a contiguous ({cols},) {dtype} tensor on {device}")
+    return bias.data_ptr()
+
+
+def _fused_slices(slices, device):
+    arr = (FusedSliceDesc * max(1, len(slices)))()
+    for i, (a, b, off) in enumerate(slices):
+        if a.device != device or b.device != device:
+            raise ValueError(f"slice {i} must be on {device}")
+        arr[i] = FusedSliceDesc(_stack_a(a, f"slice {i} lora_a"), _stack(b, f"slice {i} lora_b"),
+                                int(off))
+    return arr
+
+
 def sgmv_lora_linear(inputs, weight, slices: Sequence[Tuple[object, object, int]], output_tensor,
                      b_seq_start_loc, seq_len_tensor, lora_indices_tensor, batches: int,
                      max_seq_length: int, scaling: float = 1.0, bias=None,
@@ -519,19 +566,8 @@ def sgmv_lora_linear(inputs, weight, slices: Sequence[Tuple[object, object, int]
     x = _matrix(inputs, "inputs")
     w = _matrix(weight, "weight")
     out = _matrix(output_tensor, "output_tensor")
-    bias_ptr = None
-    if bias is not None:
-        if bias.device != device or bias.dim() != 1 or bias.shape[0] != w.rows or \
-                bias.dtype != weight.dtype or not bias.is_contiguous():
-            raise ValueError(f"bias must be a contiguous ({w.rows},) {weight.dtype} tensor on "
-                             f"{device}")
-        bias_ptr = bias.data_ptr()
-    arr = (FusedSliceDesc * max(1, len(slices)))()
-    for i, (a, b, off) in enumerate(slices):
-        if a.device != device or b.device != device:
-            raise ValueError(f"slice {i} must be on {device}")
-        arr[i] = FusedSliceDesc(_stack_a(a, f"slice {i} lora_a"), _stack(b, f"slice {i} lora_b"),
-                                int(off))
+    bias_ptr = _bias(bias, w.rows, weight.dtype, device)
+    arr = _fused_slices(slices, device)
     need = 0
     if slices and batches > 0 and workspace is None:
         need = lora_linear_workspace_bytes(x.rows, len(slices), arr[0].lora_a.rows)
@@ -647,6 +683,152 @@ def sgmv_combine(expert_rows, weights, slots, output_tensor, add_inputs: bool = 
     return output_tensor
 
 
+def mx_row_bytes(hidden: int) -> Tuple[int, int]:
+    """Bytes of codes and of scales that a row of `hidden` values takes in
+    microscaled 4-bit form: 64 and 4 for every group of 128."""
+    groups = -(-int(hidden) // 128)
+    return 64 * groups, 4 * groups
+
+
+def _mx_stack(codes, scales, hidden: int, what: str, device, dims: int) -> MxStack:
+    """codes and scales, (rows, bytes) or (matrices, rows, bytes) of uint8, as
+    rows of `hidden` values."""
+    for t, n, need in zip((codes, scales), ("codes", "scales"), mx_row_bytes(hidden)):
+        if t.device != device:
+            raise ValueError(f"{what} {n} must be on {device}")
+        if t.dtype != _torch.uint8 or t.dim() != dims or t.shape[-1] != need:
+            raise ValueError(f"{what} {n} must be {dims}-D uint8 with {need} bytes a row of {hidden} "
+                             f"values, got {tuple(t.shape)} {t.dtype}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1 or (dims == 3 and not t.is_contiguous()):
+            raise ValueError(f"{what} {n} must have contiguous " + ("matrices" if dims == 3 else "rows"))
+    if codes.shape[:-1] != scales.shape[:-1]:
+        raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} differ "
+                         "in rows")
+    strides = [t.stride(-2) if t.shape[-2] > 1 or dims == 3 else t.shape[-1] for t in (codes, scales)]
+    return MxStack(codes.data_ptr(), scales.data_ptr(), codes.shape[0] if dims == 3 else 1,
+                   codes.shape[-2], int(hidden), *strides)
+
+
+def sgmv_mx_quantize(inputs, codes, scales):
+    """Rows as microscaled 4-bit values, in place: codes (rows, 64 G) and scales
+    (rows, 4 G), uint8, G = ceil(hidden / 128) (mx_row_bytes), from inputs
+    (rows, hidden) float16, bfloat16 or float32.  32 values of a row share the
+    scale 2^(floor(log2 of the largest) - 2), byte exponent + 127, and take the
+    nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 of it (ties to the even code, the even
+    value in a byte's low half); 255 marks a block with an infinity or NaN.
+    Enqueued on the current stream."""
+    device, _ = _common(inputs, ())
+    x = _matrix(inputs, "inputs")
+    q = _mx_stack(codes, scales, x.cols, "output", device, 2)
+    rc = _call_on(device, lib.sgmv_mx_quantize, x, q, _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return codes, scales
+
+
+def sgmv_mx_dequantize(codes, scales, output_tensor, row_indices_tensor=None):
+    """output_tensor[t] = the values of row row_indices_tensor[t] (None: row t)
+    of codes and scales; indices outside their rows give rows of zeros.
+    Enqueued on the current stream."""
+    device, kept = _common(output_tensor, () if row_indices_tensor is None else
+                           [(row_indices_tensor, "row_indices_tensor")])
+    out = _matrix(output_tensor, "output_tensor")
+    if kept and kept[0].shape[0] < out.rows:
+        raise ValueError("row_indices_tensor shorter than the number of output rows")
+    q = _mx_stack(codes, scales, out.cols, "input", device, 2)
+    rc = _call_on(device, lib.sgmv_mx_dequantize, q, kept[0].data_ptr() if kept else None, out,
+                  _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return output_tensor
+
+
+def mx_lora_linear_workspace_bytes(tokens: int, hidden: int, num_slices: int = 0, rank: int = 0) -> int:
+    """Bytes of the workspace sgmv_mx_lora_linear takes."""
+    return _bytes_of(lib.sgmv_mx_lora_linear_workspace_bytes, int(tokens), int(hidden), int(num_slices),
+                     int(rank))
+
+
+def mx_grouped_gemm_workspace_bytes(input_rows: int, hidden: int) -> int:
+    """Bytes of the workspace sgmv_mx_grouped_gemm takes."""
+    return _bytes_of(lib.sgmv_mx_grouped_gemm_workspace_bytes, int(input_rows), int(hidden))
+
+
+def sgmv_mx_lora_linear(inputs, weight_codes, weight_scales, slices: Sequence[Tuple[object, object, int]],
+                        output_tensor, b_seq_start_loc, seq_len_tensor, lora_indices_tensor,
+                        batches: int, max_seq_length: int, scaling: float = 1.0, bias=None,
+                        add_inputs: bool = False, workspace=None):
+    """sgmv_lora_linear with a microscaled 4-bit weight (sgmv_mx_quantize's
+    codes (columns, 64 G) and scales (columns, 4 G)): the shared projection
+    multiplies the 4-bit values of the inputs, quantised within the call, with
+    those of the weight; the adapters read the inputs as they are.  Enqueued on
+    the current stream.  `workspace`: a uint8 tensor of
+    mx_lora_linear_workspace_bytes(), or None (taken from torch's allocator for
+    the call)."""
+    if len(slices) > MAX_SLICES:
+        raise ValueError(f"at most {MAX_SLICES} slices, got {len(slices)}")
+    device, (start, lens, idx) = _common(output_tensor, [
+        (b_seq_start_loc, "b_seq_start_loc"), (seq_len_tensor, "seq_len_tensor"),
+        (lora_indices_tensor, "lora_indices_tensor")])
+    if inputs.device != device:
+        raise ValueError(f"inputs must be on {device}")
+    if start.shape[0] < batches or lens.shape[0] < batches or idx.shape[0] < batches:
+        raise ValueError("segment metadata shorter than batches")
+    x = _matrix(inputs, "inputs")
+    w = _mx_stack(weight_codes, weight_scales, x.cols, "weight", device, 2)
+    out = _matrix(output_tensor, "output_tensor")
+    bias_ptr = _bias(bias, w.rows, inputs.dtype, device)
+    arr = _fused_slices(slices, device)
+    need = 0
+    if workspace is None:
+        adapted = slices and batches > 0
+        need = mx_lora_linear_workspace_bytes(x.rows, x.cols, len(slices) if adapted else 0,
+                                              arr[0].lora_a.rows if adapted else 0)
+    keep, ws, ws_bytes = _scratch(device, workspace, need)
+    rc = _call_on(device, lib.sgmv_mx_lora_linear, x, w, bias_ptr, arr, len(slices), out,
+                  start.data_ptr(), lens.data_ptr(), idx.data_ptr(), int(batches),
+                  int(max_seq_length), float(scaling), int(bool(add_inputs)), ws, ws_bytes,
+                  _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return output_tensor
+
+
+def sgmv_mx_grouped_gemm(inputs, expert_codes, expert_scales, output_tensor, b_seq_start_loc,
+                         seq_len_tensor, expert_indices_tensor, batches: int, max_seq_length: int,
+                         row_indices_tensor=None, gated: bool = False, workspace=None):
+    """sgmv_grouped_gemm with microscaled 4-bit experts, expert_codes (experts,
+    columns, 64 G) and expert_scales (experts, columns, 4 G); the inputs are
+    quantised within the call.  Enqueued on the current stream.  `workspace`:
+    a uint8 tensor of mx_grouped_gemm_workspace_bytes(), or None (taken from
+    torch's allocator for the call)."""
+    metas = [(b_seq_start_loc, "b_seq_start_loc"), (seq_len_tensor, "seq_len_tensor")]
+    if expert_indices_tensor is not None:
+        metas.append((expert_indices_tensor, "expert_indices_tensor"))
+    device, kept = _common(output_tensor, metas)
+    if any(m.shape[0] < batches for m in kept):
+        raise ValueError("segment metadata shorter than batches")
+    if inputs.device != device:
+        raise ValueError(f"inputs must be on {device}")
+    x = _matrix(inputs, "inputs")
+    w = _mx_stack(expert_codes, expert_scales, x.cols, "expert", device, 3)
+    out = _matrix(output_tensor, "output_tensor")
+    rows = None
+    if row_indices_tensor is not None:
+        rows = _meta(row_indices_tensor, "row_indices_tensor", device)
+        if rows.shape[0] < out.rows:
+            raise ValueError("row_indices_tensor shorter than the number of output rows")
+    need = mx_grouped_gemm_workspace_bytes(x.rows, x.cols) if workspace is None else 0
+    keep, ws, ws_bytes = _scratch(device, workspace, need)
+    rc = _call_on(device, lib.sgmv_mx_grouped_gemm, x, w, out,
+                  None if rows is None else rows.data_ptr(), kept[0].data_ptr(),
+                  kept[1].data_ptr(), kept[2].data_ptr() if len(kept) > 2 else None, int(batches),
+                  int(max_seq_length), int(bool(gated)), ws, ws_bytes, _stream(device))
+    if rc != SGMV_OK:
+        _raise(rc)
+    return output_tensor
+
+
 def abi_version() -> int:
     return lib.sgmv_abi_version()
 
@@ -655,6 +837,8 @@ __all__ = ["sgmv_expand_slice", "sgmv_expand_multi_slice", "bgmv_expand_slice", 
            "shrink_workspace_bytes", "sgmv_shrink_multi_slice_noalloc",
            "sgmv_shrink_multi_slice", "sgmv_fused_shrink_expand", "sgmv_lora_linear", "lora_linear_workspace_bytes",
            "sgmv_grouped_gemm", "sgmv_route", "route_workspace_bytes", "sgmv_combine",
-           "abi_version", "SgmvError",
-           "lib", "Matrix", "Stack", "SliceDesc", "ShrinkSliceDesc", "FusedSliceDesc",
+           "mx_row_bytes", "sgmv_mx_quantize", "sgmv_mx_dequantize", "sgmv_mx_lora_linear",
+           "mx_lora_linear_workspace_bytes", "sgmv_mx_grouped_gemm",
+           "mx_grouped_gemm_workspace_bytes", "abi_version", "SgmvError",
+           "lib", "MxStack", "Matrix", "Stack", "SliceDesc", "ShrinkSliceDesc", "FusedSliceDesc",
            "EXPORTED_SYMBOLS", "LIBRARY_PATH"]

@@ -5,6 +5,7 @@ helpers in csrc/sgmv_host.cpp) and the gfx950
 kernels (csrc/sgmv_fast_ks*.hip, csrc/sgmv_generic.hip, built from
 csrc/sgmv_device.h; csrc/sgmv_shrink_*.hip, built from csrc/sgmv_shrink.h;
 csrc/sgmv_matmul_*.hip, built from csrc/sgmv_matmul.h; csrc/sgmv_route.hip;
+csrc/sgmv_mx.hip, built from csrc/sgmv_mx.h;
 all on csrc/sgmv_common.h)
 with the code object embedded; nothing is
 compiled at run time.  Packed-fp32 VALU instructions are disabled for every
@@ -33,7 +34,8 @@ SOURCES = [os.path.join(CSRC, f) for f in
             "sgmv_fused_api.cpp", "sgmv_fused_k1.hip", "sgmv_fused_k2.hip", "sgmv_fused_k4.hip",
             "sgmv_fused_k8.hip", "sgmv_valu.hip", "sgmv_matmul_api.cpp",
             "sgmv_matmul_generic.hip", "sgmv_matmul_large.hip", "sgmv_matmul_medium.hip",
-            "sgmv_matmul_skinny.hip", "sgmv_route_api.cpp", "sgmv_route.hip")]
+            "sgmv_matmul_skinny.hip", "sgmv_route_api.cpp", "sgmv_route.hip",
+            "sgmv_mx_api.cpp", "sgmv_mx.hip")]
 
 STREAM_SOURCE = os.path.join(CSRC, "sgmv_stream.hip")
 STREAM_LIBRARY = os.path.join(HERE, "libsgmv_stream.so")

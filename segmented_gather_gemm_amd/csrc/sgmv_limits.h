@@ -154,5 +154,26 @@ constexpr int64_t shrink_workspace_bytes(int64_t C) {
   return shrink_workspace_counter_bytes(C) + C * int64_t(kShrinkPartBytes);
 }
 
+// Division of n < 2^31 by an invariant d (1 <= d < 2^31) as a 32-bit high
+// product, an addition and a shift (Granlund and Montgomery 1994): with
+// shift = ceil(log2 d) and mul = floor(2^32 (2^shift - d) / d) + 1,
+// n / d = (mulhi(mul, n) + n) >> shift; the sum stays below 2^32.
+struct Divisor {
+  uint32_t mul, shift;
+};
+constexpr Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  return Divisor{uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1), s};
+}
+constexpr uint32_t divide(uint32_t n, const Divisor& d) {
+  return (uint32_t((uint64_t(d.mul) * n) >> 32) + n) >> d.shift;
+}
+
+// Rows of microscaled 4-bit values: groups of 128 (four blocks of 32, the
+// length of a matrix instruction), 64 bytes of codes and 4 of scales each.
+constexpr int64_t mx_groups(int64_t values) { return (values + 127) / 128; }
+constexpr int64_t kMxCodeBytes = 64, kMxScaleBytes = 4;
+
 }  // namespace limits
 }  // namespace sgmv

@@ -1,6 +1,7 @@
 // sgmv_matmul_api.cpp -- libsgmv C entry points of the shared projection
 // with the adapters of many requests (sgmv_lora_linear) and of the products
-// grouped by expert (sgmv_grouped_gemm): argument checks, kernel choice, grid
+// grouped by expert (sgmv_grouped_gemm), and of both with microscaled 4-bit
+// weights (sgmv_mx_*): argument checks, kernel choice, grid
 // sizing and launch.  No allocation, no synchronisation, no device-to-host
 // traffic.
 #include <stdint.h>
@@ -9,6 +10,8 @@
 #include "sgmv_host.h"
 #include "sgmv_limits.h"
 #include "sgmv_matmul_launch.h"
+#include "sgmv_mx_host.h"
+#include "sgmv_mx_launch.h"
 
 namespace {
 
@@ -90,7 +93,7 @@ sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int 
 sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan) {
   using namespace sgmv;
   const int mode = gated ? 2 : p.grouped ? 1 : p.num_slices > 0 ? 3 : 0;
-  if (tiled_fits(p)) {
+  if (!p.ws && tiled_fits(p)) {
     int cus = 0;
     const hipError_t e = device_compute_units(&cus);
     if (e != hipSuccess)
@@ -123,7 +126,7 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
     const TiledKernel k = few ? f : pick_tiled(p, wd, mode, cus);
     *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0};
   } else {
-    *plan = Plan{matmul_generic_kernel(wd, gated), kGenericRows, kGenericCols, kThreads, 0, 0};
+    *plan = Plan{matmul_generic_kernel(wd, gated, p.ws != nullptr), kGenericRows, kGenericCols, kThreads, 0, 0};
   }
   if (!plan->kernel) return fail(SGMV_ERR_UNSUPPORTED, "no kernel for this dtype combination");
   // Grouped: at most ceil(T / rows) + min(batches, T) row tiles.
@@ -156,58 +159,17 @@ int64_t projected_bytes(int64_t tokens, int64_t rank) {
   return (tokens * projected_stride(rank) * 4 + 255) / 256 * 256;
 }
 
-}  // namespace
 
-extern "C" {
-
-sgmv_status sgmv_lora_linear_workspace_bytes(int64_t tokens, int num_slices, int64_t rank,
-                                             size_t* bytes) {
-  if (!bytes) return fail(SGMV_ERR_INVALID_ARGUMENT, "bytes pointer is null");
-  if (tokens < 0 || num_slices < 0 || num_slices > SGMV_MAX_SLICES || rank < 0)
-    return fail(SGMV_ERR_INVALID_ARGUMENT, "tokens, num_slices (<= %d) and rank must be >= 0",
-                SGMV_MAX_SLICES);
-  if (tokens > INT32_MAX || rank > SGMV_MAX_RANK)
-    return fail(SGMV_ERR_UNSUPPORTED, "tokens exceed 2^31-1 or the rank %d", SGMV_MAX_RANK);
-  *bytes = (size_t)(num_slices * projected_bytes(tokens, rank));
-  g_error.clear();
-  return SGMV_OK;
-}
-
-sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void* bias,
-                             const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
-                             const int64_t* b_seq_start_loc, const int64_t* seq_lens,
-                             const int64_t* lora_indices, int64_t batches, int64_t max_seq_len,
-                             float scale, int add_inputs, void* workspace,
-                             size_t workspace_bytes, hipStream_t stream) {
-  using namespace sgmv;
-  if (num_slices < 0 || num_slices > SGMV_MAX_SLICES)
-    return fail(SGMV_ERR_INVALID_ARGUMENT, "num_slices must be in 0..%d, got %d", SGMV_MAX_SLICES,
-                num_slices);
-  if (num_slices > 0 && !slices) return fail(SGMV_ERR_INVALID_ARGUMENT, "slices pointer is null");
-  const sgmv_matrix& x = inputs;
-  sgmv_status st = check_inputs(x, out);
-  if (st != SGMV_OK) return st;
-  if (out.rows != x.rows)
-    return fail(SGMV_ERR_INVALID_ARGUMENT, "output must have the inputs' %lld rows",
-                (long long)x.rows);
-  if (!known_dtype(weight.dtype))
-    return fail(SGMV_ERR_INVALID_ARGUMENT, "unknown weight dtype %d", weight.dtype);
-  if (weight.dtype == SGMV_F32 || x.dtype != weight.dtype)
-    return fail(SGMV_ERR_UNSUPPORTED, "inputs and weight must share one 16-bit dtype");
-  if (weight.cols != x.cols || weight.rows != out.cols || weight.row_stride < weight.cols)
-    return fail(SGMV_ERR_INVALID_ARGUMENT,
-                "weight (%lld, %lld) with row stride %lld must be (output columns %lld, hidden %lld)",
-                (long long)weight.rows, (long long)weight.cols, (long long)weight.row_stride,
-                (long long)out.cols, (long long)x.cols);
-  st = check_segments(batches, max_seq_len);
-  if (st != SGMV_OK) return st;
-
+// The adapter slices of a projection of `x` (weights of dtype wd) into `out`:
+// their rank and number of adapters.
+sgmv_status check_slices(const sgmv_fused_slice* slices, int num_slices, const sgmv_matrix& x,
+                         const sgmv_matrix& out, int wd, int64_t* rank, int64_t* lora_num) {
   int64_t K = 0, L = 0;
   for (int i = 0; i < num_slices; ++i) {
     const sgmv_fused_slice& s = slices[i];
     if (!known_dtype(s.lora_a.dtype) || !known_dtype(s.lora_b.dtype))
       return fail(SGMV_ERR_INVALID_ARGUMENT, "slice %d: unknown dtype", i);
-    if (s.lora_a.dtype != weight.dtype || s.lora_b.dtype != weight.dtype)
+    if (s.lora_a.dtype != wd || s.lora_b.dtype != wd)
       return fail(SGMV_ERR_UNSUPPORTED, "slice %d: lora_a and lora_b must have the weight's dtype",
                   i);
     if (s.lora_a.num < 0 || s.lora_a.rows < 1 || s.lora_a.cols != x.cols)
@@ -239,6 +201,146 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
   if (L > INT32_MAX) return fail(SGMV_ERR_UNSUPPORTED, "lora_num exceeds 2^31-1");
   if (K > SGMV_MAX_RANK)
     return fail(SGMV_ERR_UNSUPPORTED, "rank %lld exceeds %d", (long long)K, SGMV_MAX_RANK);
+  *rank = K;
+  *lora_num = L;
+  return SGMV_OK;
+}
+
+sgmv_status check_num_slices(const sgmv_fused_slice* slices, int num_slices) {
+  if (num_slices < 0 || num_slices > SGMV_MAX_SLICES)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "num_slices must be in 0..%d, got %d", SGMV_MAX_SLICES,
+                num_slices);
+  if (num_slices > 0 && !slices) return fail(SGMV_ERR_INVALID_ARGUMENT, "slices pointer is null");
+  return SGMV_OK;
+}
+
+// The pointers that adapters need.
+sgmv_status check_adapters(const sgmv_fused_slice* slices, int num_slices, const int64_t* start,
+                           const int64_t* lens, const int64_t* idx) {
+  if (!start || !lens || !idx)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "segment metadata pointer is null");
+  for (int i = 0; i < num_slices; ++i)
+    if (!slices[i].lora_a.data || (slices[i].lora_b.rows > 0 && !slices[i].lora_b.data))
+      return fail(SGMV_ERR_INVALID_ARGUMENT, "slice %d: null data pointer", i);
+  return SGMV_OK;
+}
+
+sgmv_status check_workspace(const void* workspace, size_t workspace_bytes, size_t need) {
+  if (!workspace || workspace_bytes < need || !aligned16(workspace))
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "workspace must be 16-byte aligned and hold %zu bytes, got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  return SGMV_OK;
+}
+
+// The adapters as p's further factors and as the slices of their projection
+// (down), whose rows lie in `workspace`.
+void attach_adapters(sgmv::MatmulParams& p, const sgmv_fused_slice* slices, int num_slices, int64_t K,
+                     int64_t L, const int64_t* start, const int64_t* lens, const int64_t* idx,
+                     int64_t batches, void* workspace, sgmv_shrink_slice* down) {
+  p.start = start;
+  p.lens = lens;
+  p.idx = idx;
+  p.batches = (int32_t)batches;
+  p.L = (int32_t)L;
+  p.K = (int32_t)K;
+  p.v_stride = (int32_t)projected_stride(K);
+  for (int i = 0; i < num_slices; ++i) {
+    if (slices[i].lora_b.rows == 0) continue;  // no column (and maybe no data)
+    const int j = p.num_slices++;
+    float* v = reinterpret_cast<float*>(static_cast<char*>(workspace) + j * projected_bytes(p.T, K));
+    down[j].lora_a = slices[i].lora_a;
+    down[j].out = sgmv_matrix{v, SGMV_F32, p.T, K, p.v_stride};
+    p.s[j] = sgmv::AdapterDesc{slices[i].lora_b.data, v, slices[i].lora_b.rows, slices[i].slice_offset};
+  }
+}
+
+// Rows quantised in a workspace: their codes, then their scales.
+struct Quantised {
+  int64_t code_stride, scale_stride, scales_at, bytes;
+};
+Quantised quantised(int64_t rows, int64_t cols) {
+  const int64_t g = sgmv::limits::mx_groups(cols);
+  Quantised q;
+  q.code_stride = g * sgmv::limits::kMxCodeBytes;
+  q.scale_stride = g * sgmv::limits::kMxScaleBytes;
+  q.scales_at = (rows * q.code_stride + 255) / 256 * 256;
+  q.bytes = q.scales_at + (rows * q.scale_stride + 255) / 256 * 256;
+  return q;
+}
+
+// Rows and columns that a workspace is sized for: as many as the quantisation
+// of a call's inputs takes.
+sgmv_status check_quantised(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "rows must be >= 0 and hidden >= 1");
+  if (cols > INT32_MAX - 4096 || rows > sgmv::kMxMaxItems / sgmv::limits::mx_groups(cols))
+    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^30 groups of 128 inputs");
+  return SGMV_OK;
+}
+
+// p's factors as microscaled rows: the weights' (checked) and the inputs',
+// which lie quantised in `workspace`.
+void attach_mx(sgmv::MatmulParams& p, const sgmv_mx_stack& w, const Quantised& q, void* workspace) {
+  p.x = workspace;
+  p.xs = static_cast<char*>(workspace) + q.scales_at;
+  p.x_row_bytes = q.code_stride;
+  p.xs_row_bytes = q.scale_stride;
+  p.w = w.codes;
+  p.ws = w.scales;
+  p.w_row_bytes = w.code_stride;
+  p.ws_row_bytes = w.scale_stride;
+  p.w_mat_bytes = w.rows * w.code_stride;
+  p.H = (int32_t)(q.code_stride / 2);
+}
+
+}  // namespace
+
+extern "C" {
+
+sgmv_status sgmv_lora_linear_workspace_bytes(int64_t tokens, int num_slices, int64_t rank,
+                                             size_t* bytes) {
+  if (!bytes) return fail(SGMV_ERR_INVALID_ARGUMENT, "bytes pointer is null");
+  if (tokens < 0 || num_slices < 0 || num_slices > SGMV_MAX_SLICES || rank < 0)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "tokens, num_slices (<= %d) and rank must be >= 0",
+                SGMV_MAX_SLICES);
+  if (tokens > INT32_MAX || rank > SGMV_MAX_RANK)
+    return fail(SGMV_ERR_UNSUPPORTED, "tokens exceed 2^31-1 or the rank %d", SGMV_MAX_RANK);
+  *bytes = (size_t)(num_slices * projected_bytes(tokens, rank));
+  g_error.clear();
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void* bias,
+                             const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
+                             const int64_t* b_seq_start_loc, const int64_t* seq_lens,
+                             const int64_t* lora_indices, int64_t batches, int64_t max_seq_len,
+                             float scale, int add_inputs, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+  using namespace sgmv;
+  const sgmv_matrix& x = inputs;
+  sgmv_status st = check_num_slices(slices, num_slices);
+  if (st != SGMV_OK) return st;
+  st = check_inputs(x, out);
+  if (st != SGMV_OK) return st;
+  if (out.rows != x.rows)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "output must have the inputs' %lld rows",
+                (long long)x.rows);
+  if (!known_dtype(weight.dtype))
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "unknown weight dtype %d", weight.dtype);
+  if (weight.dtype == SGMV_F32 || x.dtype != weight.dtype)
+    return fail(SGMV_ERR_UNSUPPORTED, "inputs and weight must share one 16-bit dtype");
+  if (weight.cols != x.cols || weight.rows != out.cols || weight.row_stride < weight.cols)
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "weight (%lld, %lld) with row stride %lld must be (output columns %lld, hidden %lld)",
+                (long long)weight.rows, (long long)weight.cols, (long long)weight.row_stride,
+                (long long)out.cols, (long long)x.cols);
+  st = check_segments(batches, max_seq_len);
+  if (st != SGMV_OK) return st;
+
+  int64_t K = 0, L = 0;
+  st = check_slices(slices, num_slices, x, out, weight.dtype, &K, &L);
+  if (st != SGMV_OK) return st;
   if (x.rows == 0 || out.cols == 0) {
     g_error.clear();
     return SGMV_OK;  // nothing to do
@@ -247,16 +349,10 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
     return fail(SGMV_ERR_INVALID_ARGUMENT, "null data pointer");
   const bool adapters = num_slices > 0 && batches > 0 && L > 0;
   if (adapters) {
-    if (!b_seq_start_loc || !seq_lens || !lora_indices)
-      return fail(SGMV_ERR_INVALID_ARGUMENT, "segment metadata pointer is null");
-    for (int i = 0; i < num_slices; ++i)
-      if (!slices[i].lora_a.data || (slices[i].lora_b.rows > 0 && !slices[i].lora_b.data))
-        return fail(SGMV_ERR_INVALID_ARGUMENT, "slice %d: null data pointer", i);
-    const size_t need = (size_t)(num_slices * projected_bytes(x.rows, K));
-    if (!workspace || workspace_bytes < need || !aligned16(workspace))
-      return fail(SGMV_ERR_INVALID_ARGUMENT,
-                  "workspace must be 16-byte aligned and hold %zu bytes, got %zu", need,
-                  workspace ? workspace_bytes : (size_t)0);
+    st = check_adapters(slices, num_slices, b_seq_start_loc, seq_lens, lora_indices);
+    if (st != SGMV_OK) return st;
+    st = check_workspace(workspace, workspace_bytes, (size_t)(num_slices * projected_bytes(x.rows, K)));
+    if (st != SGMV_OK) return st;
   }
 
   MatmulParams p{};
@@ -273,24 +369,9 @@ sgmv_status sgmv_lora_linear(sgmv_matrix inputs, sgmv_matrix weight, const void*
   p.out_dtype = out.dtype;
   p.add = add_inputs != 0;
   sgmv_shrink_slice down[SGMV_MAX_SLICES];
-  if (adapters) {
-    p.start = b_seq_start_loc;
-    p.lens = seq_lens;
-    p.idx = lora_indices;
-    p.batches = (int32_t)batches;
-    p.L = (int32_t)L;
-    p.K = (int32_t)K;
-    p.v_stride = (int32_t)projected_stride(K);
-    for (int i = 0; i < num_slices; ++i) {
-      if (slices[i].lora_b.rows == 0) continue;  // no column (and maybe no data)
-      const int j = p.num_slices++;
-      float* v = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                          j * projected_bytes(x.rows, K));
-      down[j].lora_a = slices[i].lora_a;
-      down[j].out = sgmv_matrix{v, SGMV_F32, x.rows, K, p.v_stride};
-      p.s[j] = AdapterDesc{slices[i].lora_b.data, v, slices[i].lora_b.rows, slices[i].slice_offset};
-    }
-  }
+  if (adapters)
+    attach_adapters(p, slices, num_slices, K, L, b_seq_start_loc, seq_lens, lora_indices, batches,
+                    workspace, down);
   Plan plan;
   st = make_plan(p, weight.dtype, false, &plan);
   if (st != SGMV_OK) return st;
@@ -360,6 +441,162 @@ sgmv_status sgmv_grouped_gemm(sgmv_matrix inputs, sgmv_stack weights, sgmv_matri
   Plan plan;
   st = make_plan(p, weights.dtype, gated != 0, &plan);
   if (st != SGMV_OK) return st;
+  return launch(plan, p, stream);
+}
+
+sgmv_status sgmv_mx_lora_linear_workspace_bytes(int64_t tokens, int64_t hidden, int num_slices,
+                                                int64_t rank, size_t* bytes) {
+  size_t adapters = 0;
+  sgmv_status st = sgmv_lora_linear_workspace_bytes(tokens, num_slices, rank, bytes ? &adapters : nullptr);
+  if (st != SGMV_OK) return st;
+  st = check_quantised(tokens, hidden);
+  if (st != SGMV_OK) return st;
+  *bytes = (size_t)quantised(tokens, hidden).bytes + adapters;
+  g_error.clear();
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_mx_lora_linear(sgmv_matrix inputs, sgmv_mx_stack weight, const void* bias,
+                                const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
+                                const int64_t* b_seq_start_loc, const int64_t* seq_lens,
+                                const int64_t* lora_indices, int64_t batches, int64_t max_seq_len,
+                                float scale, int add_inputs, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  using namespace sgmv;
+  const sgmv_matrix& x = inputs;
+  sgmv_status st = check_num_slices(slices, num_slices);
+  if (st != SGMV_OK) return st;
+  st = check_inputs(x, out);
+  if (st != SGMV_OK) return st;
+  if (out.rows != x.rows)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "output must have the inputs' %lld rows",
+                (long long)x.rows);
+  if (x.dtype == SGMV_F32) return fail(SGMV_ERR_UNSUPPORTED, "inputs must have a 16-bit dtype");
+  st = check_mx(weight, x.cols, "weight");
+  if (st != SGMV_OK) return st;
+  if (weight.num != 1 || weight.rows != out.cols)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "weight must be one matrix of %lld rows, got %lld of %lld",
+                (long long)out.cols, (long long)weight.num, (long long)weight.rows);
+  st = check_segments(batches, max_seq_len);
+  if (st != SGMV_OK) return st;
+  int64_t K = 0, L = 0;
+  st = check_slices(slices, num_slices, x, out, x.dtype, &K, &L);
+  if (st != SGMV_OK) return st;
+  st = check_quantised(x.rows, x.cols);
+  if (st != SGMV_OK) return st;
+  if (x.rows == 0 || out.cols == 0) {
+    g_error.clear();
+    return SGMV_OK;  // nothing to do
+  }
+  if (!x.data || !out.data || !weight.codes || !weight.scales)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "null data pointer");
+  const bool adapters = num_slices > 0 && batches > 0 && L > 0;
+  if (adapters) {
+    st = check_adapters(slices, num_slices, b_seq_start_loc, seq_lens, lora_indices);
+    if (st != SGMV_OK) return st;
+  }
+  const Quantised q = quantised(x.rows, x.cols);
+  st = check_workspace(workspace, workspace_bytes,
+                       (size_t)(q.bytes + (adapters ? num_slices * projected_bytes(x.rows, K) : 0)));
+  if (st != SGMV_OK) return st;
+
+  MatmulParams p{};
+  p.bias = bias;
+  p.out = out.data;
+  p.out_row_bytes = out.row_stride * elem_bytes(out.dtype);
+  p.T = p.X = x.rows;
+  p.N = (int32_t)out.cols;
+  p.out_dtype = out.dtype;
+  p.add = add_inputs != 0;
+  attach_mx(p, weight, q, workspace);
+  sgmv_shrink_slice down[SGMV_MAX_SLICES];
+  if (adapters)
+    attach_adapters(p, slices, num_slices, K, L, b_seq_start_loc, seq_lens, lora_indices, batches,
+                    static_cast<char*>(workspace) + q.bytes, down);
+  Plan plan;
+  st = make_plan(p, x.dtype, false, &plan);
+  if (st != SGMV_OK) return st;
+  st = launch_mx_quantize(x, workspace, q.code_stride, static_cast<char*>(workspace) + q.scales_at,
+                          q.scale_stride, stream);
+  if (st != SGMV_OK) return st;
+  if (p.num_slices > 0) {
+    // The adapters' projections read the inputs themselves, not their 4-bit values.
+    st = sgmv_shrink_multi_slice(inputs, down, p.num_slices, b_seq_start_loc, seq_lens, lora_indices,
+                                 batches, max_seq_len, scale, nullptr, 0, stream);
+    if (st != SGMV_OK) return st;
+  }
+  return launch(plan, p, stream);
+}
+
+sgmv_status sgmv_mx_grouped_gemm_workspace_bytes(int64_t input_rows, int64_t hidden, size_t* bytes) {
+  if (!bytes) return fail(SGMV_ERR_INVALID_ARGUMENT, "bytes pointer is null");
+  const sgmv_status st = check_quantised(input_rows, hidden);
+  if (st != SGMV_OK) return st;
+  *bytes = (size_t)quantised(input_rows, hidden).bytes;
+  g_error.clear();
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_mx_grouped_gemm(sgmv_matrix inputs, sgmv_mx_stack weights, sgmv_matrix out,
+                                 const int64_t* row_indices, const int64_t* b_seq_start_loc,
+                                 const int64_t* seq_lens, const int64_t* expert_indices,
+                                 int64_t batches, int64_t max_seq_len, int gated, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+  using namespace sgmv;
+  const sgmv_matrix& x = inputs;
+  sgmv_status st = check_inputs(x, out);
+  if (st != SGMV_OK) return st;
+  if (x.dtype == SGMV_F32) return fail(SGMV_ERR_UNSUPPORTED, "inputs must have a 16-bit dtype");
+  st = check_mx(weights, x.cols, "weights");
+  if (st != SGMV_OK) return st;
+  if (weights.rows != (gated ? 2 * out.cols : out.cols))
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "weights must have %lld rows each, got %lld",
+                (long long)(gated ? 2 * out.cols : out.cols), (long long)weights.rows);
+  if (!row_indices && x.rows != out.rows)
+    return fail(SGMV_ERR_INVALID_ARGUMENT,
+                "output must have the inputs' %lld rows without row_indices", (long long)x.rows);
+  if (weights.num > INT32_MAX) return fail(SGMV_ERR_UNSUPPORTED, "experts exceed 2^31-1");
+  st = check_segments(batches, max_seq_len);
+  if (st != SGMV_OK) return st;
+  st = check_quantised(x.rows, x.cols);
+  if (st != SGMV_OK) return st;
+  if (batches == 0 || out.rows == 0 || out.cols == 0 || weights.num == 0) {
+    g_error.clear();
+    return SGMV_OK;  // nothing to do
+  }
+  if ((!x.data && x.rows > 0) || !out.data || !weights.codes || !weights.scales)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "null data pointer");
+  if (!b_seq_start_loc || !seq_lens)
+    return fail(SGMV_ERR_INVALID_ARGUMENT, "segment metadata pointer is null");
+  const Quantised q = quantised(x.rows, x.cols);
+  if (x.rows > 0) {
+    st = check_workspace(workspace, workspace_bytes, (size_t)q.bytes);
+    if (st != SGMV_OK) return st;
+  }
+
+  MatmulParams p{};
+  p.out = out.data;
+  p.start = b_seq_start_loc;
+  p.lens = seq_lens;
+  p.idx = expert_indices;
+  p.rows = row_indices;
+  p.out_row_bytes = out.row_stride * elem_bytes(out.dtype);
+  p.T = out.rows;
+  p.X = x.rows;
+  p.N = (int32_t)out.cols;
+  p.batches = (int32_t)batches;
+  p.L = (int32_t)weights.num;
+  p.grouped = 1;
+  p.out_dtype = out.dtype;
+  attach_mx(p, weights, q, workspace);
+  Plan plan;
+  st = make_plan(p, x.dtype, gated != 0, &plan);
+  if (st != SGMV_OK) return st;
+  if (x.rows > 0) {
+    st = launch_mx_quantize(x, workspace, q.code_stride, static_cast<char*>(workspace) + q.scales_at,
+                            q.scale_stride, stream);
+    if (st != SGMV_OK) return st;
+  }
   return launch(plan, p, stream);
 }
 

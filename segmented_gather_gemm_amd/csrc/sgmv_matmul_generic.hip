@@ -7,12 +7,15 @@
 // element by element where they are not.  Nothing is staged and every wave
 // reads the tile's weights again (from the caches), so this kernel is bound
 // by load latency; it is for the shapes that the tiled kernels do not take.
+// MX: operands are microscaled 4-bit rows, one group of 128 values (16 bytes
+// of codes a lane, the block's scale from the group's word) an instruction.
 #include "sgmv_matmul.h"
+#include "sgmv_mx.h"
 
 namespace sgmv {
 namespace dev {
 
-template <int WD, bool GATED>
+template <int WD, bool GATED, bool MX>
 __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
   __shared__ int32_t sh[kWaves + 4];
   __shared__ int32_t row_pos[kGenericRows], list[kGenericRows];
@@ -36,7 +39,34 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
                     (uint64_t)p.w_mat_bytes) & 15) == 0;
 
   f32x4 acc[GATED ? 2 : 1][kBlocks] = {};
-  for (int h = 0; h < p.H; h += 32) {
+  if constexpr (MX) {  // whole groups, rows and words aligned
+    const char* xs = static_cast<const char*>(p.xs) + (have ? src : 0) * p.xs_row_bytes;
+    for (int g = 0; g < p.H / 32; ++g) {
+      u32x4 xv{};
+      uint32_t sx = 0;
+      if (have) {
+        xv = *reinterpret_cast<const u32x4*>(xr + g * 64 + q * 16);
+        sx = *reinterpret_cast<const uint32_t*>(xs + g * 4) >> (8 * q);
+      }
+#pragma unroll
+      for (int f = 0; f < kBlocks; ++f) {
+        const int n = n0 + f * 16 + (lane & 15);
+#pragma unroll
+        for (int t = 0; t < (GATED ? 2 : 1); ++t) {
+          u32x4 wv{};
+          uint32_t sw = 0;
+          if (n < p.N) {
+            const int64_t r = (int64_t)t * p.N + n;
+            wv = *reinterpret_cast<const u32x4*>(wm + r * p.w_row_bytes + g * 64 + q * 16);
+            sw = *reinterpret_cast<const uint32_t*>(
+                     static_cast<const char*>(p.ws) +
+                     (loc.e * (GATED ? 2 : 1) * (int64_t)p.N + r) * p.ws_row_bytes + g * 4) >> (8 * q);
+          }
+          acc[t][f] = mfma_fp4<0>(wv, xv, acc[t][f], sw, sx);
+        }
+      }
+    }
+  } else for (int h = 0; h < p.H; h += 32) {
     const int at = h + q * 8, cnt = clamp8((int64_t)p.H - at);
     u32x4 xv;
     load_any8<WD>(xr, at, have ? cnt : 0, vx, &xv);
@@ -143,13 +173,17 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
 
 }  // namespace dev
 
-const void* matmul_generic_kernel(int wd, bool gated) {
+template <bool GATED, bool MX>
+static const void* generic_of(int wd) {
   using namespace dev;
-  if (wd == BF16)
-    return gated ? (const void*)matmul_generic<BF16, true> : (const void*)matmul_generic<BF16, false>;
-  if (wd == F16)
-    return gated ? (const void*)matmul_generic<F16, true> : (const void*)matmul_generic<F16, false>;
-  return nullptr;
+  return wd == BF16  ? (const void*)matmul_generic<BF16, GATED, MX>
+         : wd == F16 ? (const void*)matmul_generic<F16, GATED, MX>
+                     : nullptr;
+}
+
+const void* matmul_generic_kernel(int wd, bool gated, bool mx) {
+  if (mx) return gated ? generic_of<true, true>(wd) : generic_of<false, true>(wd);
+  return gated ? generic_of<true, false>(wd) : generic_of<false, false>(wd);
 }
 
 }  // namespace sgmv

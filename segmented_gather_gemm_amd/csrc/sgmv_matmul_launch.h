@@ -21,6 +21,10 @@ struct AdapterDesc {
 //    adapters of the segments' rows (start, lens, idx);
 //  * grouped: the rows of segment b with weight matrix idx[b] (idx null: b).
 // The segment fields keep Params' names.
+//
+// Microscaled 4-bit operands (mx): x and w are rows of codes, H counts 16-bit
+// words of them (32 a group of 128 values), so that every offset is as for
+// 16-bit values, and xs and ws hold the scales.
 struct MatmulParams {
   const void* x;
   const void* w;
@@ -50,11 +54,15 @@ struct MatmulParams {
   int32_t K;
   int32_t v_stride;
   AdapterDesc s[kMaxSlices];
+  const void* xs;         // mx: scales of x's and of w's rows
+  const void* ws;
+  int64_t xs_row_bytes;
+  int64_t ws_row_bytes;
 };
 
 // Generic kernel: any size, stride and alignment (64 x 64 tiles).
 constexpr int kGenericRows = 64, kGenericCols = 64;
-const void* matmul_generic_kernel(int wd, bool gated);
+const void* matmul_generic_kernel(int wd, bool gated, bool mx = false);
 
 // Tiled kernels: rows of 16-byte blocks (hidden a multiple of eight, 16-byte
 // aligned rows of x and w) that 32-bit offsets reach.  mode: 0 dense, 1
