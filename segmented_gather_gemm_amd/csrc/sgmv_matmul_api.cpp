@@ -56,14 +56,16 @@ int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
 // Whether the tiled kernels' 16-byte blocks and 32-bit offsets fit: hidden a
 // multiple of eight, aligned rows, and less than 2 GiB from the first to the
 // last row of a tile (gathered inputs: of all of them); adapters of ranks that are
-// multiples of eight, aligned and less than 2 GiB each.
+// multiples of eight, aligned and less than 2 GiB each.  Microscaled rows are
+// aligned as they are; their scales have the same bounds on far shorter rows,
+// but whatever stride a caller gives them.
 bool tiled_fits(const sgmv::MatmulParams& p) {
   const int64_t most = int64_t(1) << 31, rows = 256;
   for (int i = 0; i < p.num_slices; ++i)
     if (p.K % 8 != 0 || !aligned16(p.s[i].b) || p.s[i].n * p.K * 2 >= most) return false;
   return p.H % 8 == 0 && aligned16(p.x) && aligned16(p.w) && p.x_row_bytes % 16 == 0 &&
          p.w_row_bytes % 16 == 0 && p.w_mat_bytes % 16 == 0 && rows * p.w_row_bytes < most && rows * p.out_row_bytes < most &&
-         (p.rows ? p.X : rows) * p.x_row_bytes < most;
+         (p.rows ? p.X : rows) * p.x_row_bytes < most && rows * p.ws_row_bytes < most;
 }
 
 // 256 x 256 tiles, one workgroup per compute unit, or 128 x 128 tiles, two:
@@ -78,8 +80,9 @@ bool tiled_fits(const sgmv::MatmulParams& p) {
 // are near each other (32 experts x 188 rows of the same, 124 and 121 us) it
 // may miss by 5%.  A segment fills half of its last tile on average.
 sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int cus) {
-  const sgmv::TiledKernel l = sgmv::matmul_tiled_large(wd, mode);
-  const sgmv::TiledKernel m = sgmv::matmul_tiled_medium(wd, mode);
+  const bool mx = p.ws != nullptr;
+  const sgmv::TiledKernel l = mx ? sgmv::mx_tiled_large(wd, mode) : sgmv::matmul_tiled_large(wd, mode);
+  const sgmv::TiledKernel m = mx ? sgmv::mx_tiled_medium(wd, mode) : sgmv::matmul_tiled_medium(wd, mode);
   auto count = [&](const sgmv::TiledKernel& k) {
     const int64_t rows = p.grouped ? (2 * p.T + p.batches * k.rows) / (2 * k.rows) : tiles(p.T, k.rows);
     return rows * tiles(p.N, k.cols);
@@ -93,7 +96,7 @@ sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int 
 sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan) {
   using namespace sgmv;
   const int mode = gated ? 2 : p.grouped ? 1 : p.num_slices > 0 ? 3 : 0;
-  if (!p.ws && tiled_fits(p)) {
+  if (tiled_fits(p)) {
     int cus = 0;
     const hipError_t e = device_compute_units(&cus);
     if (e != hipSuccess)
@@ -120,7 +123,7 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
                           : p.T <= 32           ? matmul_skinny_32(wd, adapted)
                                                 : matmul_skinny_64_adapted(wd);
     const int64_t used = p.batches < p.T ? p.batches : p.T;
-    const bool few = p.grouped ? tiles(p.T, p.batches) <= 16 && 2 * used * tiles(p.N, m.cols) <= cus
+    const bool few = p.ws ? false : p.grouped ? tiles(p.T, p.batches) <= 16 && 2 * used * tiles(p.N, m.cols) <= cus
                                : p.T <= 16 || (p.T <= (adapted ? 64 : 32) &&
                                                f.rows * tiles(p.N, f.cols) <= (adapted ? 160 : 80) * (int64_t)cus);
     const TiledKernel k = few ? f : pick_tiled(p, wd, mode, cus);

@@ -73,6 +73,8 @@ struct TiledKernel {
 };
 TiledKernel matmul_tiled_large(int wd, int mode);
 TiledKernel matmul_tiled_medium(int wd, int mode);
+TiledKernel mx_tiled_large(int wd, int mode);  // microscaled operands
+TiledKernel mx_tiled_medium(int wd, int mode);
 // Few rows (the same requirements): tiles of 16 rows, of 32 for dense calls
 // and of 64 for dense calls with adapters.
 TiledKernel matmul_skinny_16(int wd, int mode);

@@ -36,8 +36,10 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "sgmv_matmul.h"
+#include "sgmv_mx.h"
 
 namespace sgmv {
 namespace dev {
@@ -79,16 +81,64 @@ __device__ __forceinline__ void wait_lds_reads() {
   pin();
 }
 
-// c += a . b with c held in the accumulation registers.  Written out, because
+// c += a . b with c held in the accumulation registers (ACC; else in the
+// others).  Written out, because
 // the 256 x 256 tile's accumulators fill all 256 of them and the compiler
 // otherwise moves some of them at every step.  The compiler does not see a
 // matrix instruction here: what reads c next waits for mfma_done().
-template <int WD>
+template <int WD, bool ACC = true>
 __device__ __forceinline__ void mfma_into(f32x4& c, u32x4 a, u32x4 b) {
-  if constexpr (WD == BF16)
+  if constexpr (WD == BF16 && ACC)
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-  else
+  else if constexpr (WD == BF16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+  else if constexpr (ACC)
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+}
+
+// The same for 4-bit values, byte SEL of sa and sb the lane's scales.
+#define SGMV_MFMA_FP4(C, LO, HI)                                                              \
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[" LO "," LO  \
+               ",0] op_sel_hi:[" HI "," HI ",0] cbsz:4 blgp:4"                                \
+               : "+" C(c) : "v"(a), "v"(b), "v"(sa), "v"(sb))
+template <int SEL, bool ACC>
+__device__ __forceinline__ void mfma_fp4_into(f32x4& c, u32x4 a, u32x4 b, uint32_t sa, uint32_t sb) {
+  if constexpr (ACC) {
+    if constexpr (SEL == 0) SGMV_MFMA_FP4("a", "0", "0");
+    else if constexpr (SEL == 1) SGMV_MFMA_FP4("a", "1", "0");
+    else if constexpr (SEL == 2) SGMV_MFMA_FP4("a", "0", "1");
+    else SGMV_MFMA_FP4("a", "1", "1");
+  } else {
+    if constexpr (SEL == 0) SGMV_MFMA_FP4("v", "0", "0");
+    else if constexpr (SEL == 1) SGMV_MFMA_FP4("v", "1", "0");
+    else if constexpr (SEL == 2) SGMV_MFMA_FP4("v", "0", "1");
+    else SGMV_MFMA_FP4("v", "1", "1");
+  }
+}
+#undef SGMV_MFMA_FP4
+
+// f(0), f(1), ... f(N - 1), the numbers as constants (a loop of this many matrix
+// instructions with their scales passes the compiler's limit on unrolling).
+template <typename F, int... I>
+__device__ __forceinline__ void for_each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void for_each(F f) {
+  for_each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// Four words (groups) of four scale bytes (blocks) with rows and columns
+// exchanged: word q has the scales of block q of each group.
+__device__ __forceinline__ u32x4 transpose_bytes(u32x4 v) {
+  const uint32_t a = __builtin_amdgcn_perm(v[1], v[0], 0x05010400);  // v0.0 v1.0 v0.1 v1.1
+  const uint32_t b = __builtin_amdgcn_perm(v[3], v[2], 0x05010400);
+  const uint32_t c = __builtin_amdgcn_perm(v[1], v[0], 0x07030602);  // v0.2 v1.2 v0.3 v1.3
+  const uint32_t d = __builtin_amdgcn_perm(v[3], v[2], 0x07030602);
+  return u32x4{__builtin_amdgcn_perm(b, a, 0x05040100), __builtin_amdgcn_perm(b, a, 0x07060302),
+               __builtin_amdgcn_perm(d, c, 0x05040100), __builtin_amdgcn_perm(d, c, 0x07060302)};
 }
 
 // The larger of a lane's value and the one that DPP control CTRL (of all lanes'
@@ -120,12 +170,18 @@ __device__ __forceinline__ void mfma_done() {
   pin();
 }
 
-template <int WD, int MODE, typename S>
+template <int WD, int MODE, typename S, bool MX = false>
 __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulParams p) {
   constexpr int FM = S::FM, FN = S::FN, LL = S::kLoads, HM = S::HM, HN = S::HN;
+  constexpr int kS = MX ? (S::BM + S::BN) / S::kNT : 0;  // rows of scales a thread stages
+  // Two workgroups a compute unit leave 128 registers of either kind: with the
+  // scales more than that are wanted beside the accumulators, and the compiler
+  // would move operands between the two right ahead of their use.
+  constexpr bool kAcc = !MX || S::kOccupancy == 1;
   __shared__ uint16_t a00[HM * 64], a01[HM * 64], a10[HM * 64], a11[HM * 64];
   __shared__ uint16_t b00[HN * 64], b01[HN * 64], b10[HN * 64], b11[HN * 64];
   __shared__ int32_t sh[S::kWaves + 4];
+  __shared__ u32x4 scales[MX ? S::BM + S::BN : 1];  // input rows, then weight rows
 
   const TileLoc loc = find_tile<S::kNT>(p, S::BM, sh);
   if (loc.row < 0) return;
@@ -150,7 +206,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     for (int i = 0; i < LL; ++i) {
       const int r = h * HM + (wave * LL + i) * 8 + lr;
       int64_t src = r;
-      bool ok = r < rows;
+      bool ok = r < rows || (MX && (MODE == kDense || MODE == kAdapted));
       if (gather) {
         src = ok ? p.rows[loc.row + r] : 0;
         ok = ok && src >= 0 && src < p.X;
@@ -178,20 +234,68 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     woff[i] = (uint32_t)((int64_t)n * p.w_row_bytes) + chunk * 16;
   }
 
+  // MX: this thread's rows of scales, as staged.
+  rsrc_t sr[MX ? kS : 1];
+  uint32_t soff[MX ? kS : 1];
+  if constexpr (MX) {
+#pragma unroll
+    for (int j = 0; j < kS; ++j) {
+      const int u = threadIdx.x + j * S::kNT;
+      if (uniform(u) < S::BM) {
+        int64_t src = u;
+        bool ok = u < rows;
+        if (gather) {
+          src = ok ? p.rows[loc.row + u] : 0;
+          ok = ok && src >= 0 && src < p.X;
+        }
+        sr[j] = uniform_rsrc(static_cast<const char*>(p.xs) + (gather ? 0 : loc.row) * p.xs_row_bytes,
+                             ((gather ? p.X : rows) - 1) * p.xs_row_bytes + p.H / 8);
+        soff[j] = ok ? (uint32_t)(src * p.xs_row_bytes) : kOut;
+      } else {
+        const int q = u - S::BM, h = uniform(q) / HN, in = q % HN, blk = in / (16 * FN);
+        const int f = in % (16 * FN) / 16, r = in % 16;
+        const int n = blk * 16 * FN + (r >> 2) * 4 * FN + f * 4 + (r & 3);
+        const int64_t first = MODE == kGated ? (int64_t)h * p.N + n0 : (int64_t)n0 + h * HN;
+        const int64_t left = MODE == kGated ? p.N - n0 : (int64_t)p.N - n0 - h * HN;
+        const int64_t nr = left < HN ? left : HN;
+        constexpr int kMats = MODE == kGated ? 2 : 1;
+        sr[j] = uniform_rsrc(static_cast<const char*>(p.ws) +
+                                 (loc.e * (int64_t)kMats * p.N + first) * p.ws_row_bytes,
+                             nr <= 0 ? 0 : (nr - 1) * p.ws_row_bytes + p.H / 8);
+        soff[j] = (uint32_t)((int64_t)n * p.ws_row_bytes);
+      }
+    }
+  }
+
   const int steps = (p.H + 63) / 64;
   // Load i of half h of step t, zeros past the contraction.  The step is part
   // of the lane's offset, which alone is certain to be held against the
   // resource's end (a half of the weights may have no row at all).
+  // MX: a load's rows lie a wave-uniform distance from those of the lane's
+  // first, whose offset alone takes a register (rows that follow each other
+  // and pass the tile's end pass the resource's); the distance is worked out
+  // anew each time, or the compiler keeps the sums.
+  auto here = [](int64_t v) __attribute__((always_inline)) {
+    int32_t bytes = (int32_t)v;
+    asm volatile("" : "+s"(bytes));
+    return bytes;
+  };
   auto load_a = [&](uint16_t* dst, int h, int t, int i) __attribute__((always_inline)) {
     const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
+    const uint32_t row = MX && (MODE == kDense || MODE == kAdapted)
+                             ? xoff[0][0] + (uint32_t)((h * HM + i * 8) * here(p.x_row_bytes))
+                             : xoff[h][i];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(dst + (wave * LL + i) * 512), 16,
-                                             (int)(in ? xoff[h][i] + (uint32_t)t * 128u : kOut), 0,
+                                             (int)(in ? row + (uint32_t)t * 128u : kOut), 0,
                                              0, 0);
   };
   auto load_b = [&](uint16_t* dst, int h, int t, int i) __attribute__((always_inline)) {
     const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
+    static_assert(16 * FN % (8 * LL) == 0, "a wave's loads of a half stay within a block of rows");
+    const uint32_t row =
+        MX ? woff[0] + (uint32_t)((i / 2 * 4 + i % 2 * 8 * FN) * here(p.w_row_bytes)) : woff[i];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[h], (lds_void*)(dst + (wave * LL + i) * 512), 16,
-                                             (int)(in ? woff[i] + (uint32_t)t * 128u : kOut), 0, 0,
+                                             (int)(in ? row + (uint32_t)t * 128u : kOut), 0, 0,
                                              0);
   };
 
@@ -228,6 +332,36 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   constexpr int kEarly = S::kOccupancy == 1                    ? kLoads * 5 / 8
                          : MODE == kDense || MODE == kAdapted ? kLoads
                                                               : kLoads * 3 / 4;
+  // MX: scales come for two steps (four groups) at a time.  They are loaded
+  // during the first of the two steps before theirs, go to LDS in the second,
+  // a row's four words transposed, so that a lane reads its four groups'
+  // scales as one word, and from there into the registers of those they
+  // follow, each after its last use.  Words past the row's end, which may be
+  // another row's, become zeros.
+  u32x4 sraw[MX ? kS : 1];
+  uint32_t sa[MX ? 2 * FM : 1], sb[MX ? 2 * FN : 1];
+  auto load_scales = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kS; ++j)
+      sraw[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                              sr[j], (int)(soff[j] + (uint32_t)t * 8u), 0, 0));
+  };
+  auto store_scales = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kS; ++j) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sraw[j][w] &= 32 * (2 * t + w) < p.H ? ~0u : 0u;
+      scales[threadIdx.x + j * S::kNT] = transpose_bytes(sraw[j]);
+    }
+  };
+  auto read_sa = [&](int m) __attribute__((always_inline)) {
+    const int r = (m / FM) * HM + (wm * FM + m % FM) * 16 + orow;
+    sa[m] = reinterpret_cast<const uint32_t*>(scales + r)[oq];
+  };
+  auto read_sb = [&](int n) __attribute__((always_inline)) {
+    const int r = S::BM + (n / FN) * HN + (wn * FN + n % FN) * 16 + orow;
+    sb[n] = reinterpret_cast<const uint32_t*>(scales + r)[oq];
+  };
   // Step t, whose operands are in sets 0 and 1 + t % 2, with its LDS
   // (A0, A1, B0, B1) free and the next step's in (C0, C1, D0, D1).  BOTH:
   // whether the second A half holds any row.
@@ -236,25 +370,51 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
                   auto both) __attribute__((always_inline)) {
     constexpr int kRows = decltype(both)::value ? 2 * FM : FM;
     constexpr int kMfma = kRows * 2 * FN, kSet = decltype(set)::value;
-    auto rows_of = [&](int from, auto between) __attribute__((always_inline)) {
+    auto rows_of = [&](auto part, int from, auto between) __attribute__((always_inline)) {
+      if constexpr (MX) {
+        constexpr int kSel = 2 * (kSet - 1) + decltype(part)::value;
+        for_each<kMfma>([&](auto at) __attribute__((always_inline)) {
+          constexpr int k = decltype(at)::value, m = k / (2 * FN), n = k % (2 * FN);
+          between(k);
+          mfma_fp4_into<kSel, kAcc>(acc[m / FM][n / FN][m % FM][n % FN], wb[from][n], xa[from][m], sb[n],
+                              sa[m]);
+          if constexpr (kSel == 3) {  // the last use of these scales
+            pin();
+            if constexpr (n == 2 * FN - 1) read_sa(m);
+            if constexpr (m == kRows - 1) read_sb(n);
+            pin();
+          }
+        });
+      } else {
 #pragma unroll
-      for (int k = 0; k < kMfma; ++k) {
-        const int m = k / (2 * FN), n = k % (2 * FN);
-        between(k);
-        mfma_into<WD>(acc[m / FM][n / FN][m % FM][n % FN], wb[from][n], xa[from][m]);
+        for (int k = 0; k < kMfma; ++k) {
+          const int m = k / (2 * FN), n = k % (2 * FN);
+          between(k);
+          mfma_into<WD, kAcc>(acc[m / FM][n / FN][m % FM][n % FN], wb[from][n], xa[from][m]);
+        }
       }
     };
     int loads = 0, reads = 0;
-    rows_of(0, [&](int k) __attribute__((always_inline)) {
+    rows_of(std::integral_constant<int, 0>{}, 0, [&](int k) __attribute__((always_inline)) {
       if (loads * kMfma <= k * kEarly && loads < kEarly) {
         pin();
         load_one(A0, A1, B0, B1, t + 2, loads++);
         pin();
       }
     });
-    wait_loads<kEarly>();
+    if constexpr (MX && kSet == 1) {
+      pin();
+      load_scales(t + 2);
+      wait_loads<kEarly + kS>();
+    } else {
+      wait_loads<kEarly>();
+    }
+    if constexpr (MX && kSet == 2) {
+      store_scales(t + 1);
+      wait_lds_reads();
+    }
     wg_barrier();
-    rows_of(kSet, [&](int k) __attribute__((always_inline)) {
+    rows_of(std::integral_constant<int, 1>{}, kSet, [&](int k) __attribute__((always_inline)) {
       if ((loads - kEarly) * kMfma <= k * (kLoads - kEarly) && loads < kLoads) {
         pin();
         load_one(A0, A1, B0, B1, t + 2, loads++);
@@ -279,6 +439,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     seg = read_segment(p, threadIdx.x);
     pin();  // ahead of the loads into LDS: loads arrive in order
   }
+  if constexpr (MX) {
+    load_scales(0);
+    pin();  // ahead of the loads into LDS too
+  }
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) load_one(a00, a01, b00, b01, 0, i);
 #pragma unroll
@@ -299,7 +463,17 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     tile_adapters<S::kNT, S::BM, false>(p, seg, loc.row, loc.end, row_pos, list, count, segs);
   }
   wait_loads<kLoads>();
+  if constexpr (MX) {
+    store_scales(0);
+    wait_lds_reads();
+  }
   wg_barrier();
+  if constexpr (MX) {
+#pragma unroll
+    for (int m = 0; m < 2 * FM; ++m) read_sa(m);
+#pragma unroll
+    for (int n = 0; n < 2 * FN; ++n) read_sb(n);
+  }
 #pragma unroll
   for (int i = 0; i < 2 * kReads; ++i)
     read_one(a00, a01, b00, b01, i / kReads, i / kReads, i % kReads);
@@ -372,10 +546,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
           // The copy is made here and goes back before the next one's: the
           // compiler would hold all of them in vector registers otherwise.
           f32x4& c = acc[m / FM][n / FN][m % FM][n % FN];
-          asm volatile("" : "+a"(c));
+          if constexpr (kAcc) asm volatile("" : "+a"(c));
 #pragma unroll
           for (int j = 0; j < 4; ++j) c[j] = ldexpf(c[j], by[m]);
-          asm volatile("" : "+a"(c));
+          if constexpr (kAcc) asm volatile("" : "+a"(c));
           pin();
         }
       mfma_ready();
@@ -514,7 +688,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
                 mfma_ready();
 #pragma unroll
                 for (int n = 0; n < 2 * FN; ++n)
-                  mfma_into<WD>(acc[m / FM][n / FN][m % FM][n % FN], wb[0][n], x);
+                  mfma_into<WD, kAcc>(acc[m / FM][n / FN][m % FM][n % FN], wb[0][n], x);
               }
             }
           }
