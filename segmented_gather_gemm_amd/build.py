@@ -35,7 +35,8 @@ SOURCES = [os.path.join(CSRC, f) for f in
             "sgmv_fused_k8.hip", "sgmv_valu.hip", "sgmv_matmul_api.cpp",
             "sgmv_matmul_generic.hip", "sgmv_matmul_large.hip", "sgmv_matmul_medium.hip",
             "sgmv_matmul_skinny.hip", "sgmv_route_api.cpp", "sgmv_route.hip",
-            "sgmv_mx_api.cpp", "sgmv_mx.hip", "sgmv_mx_large.hip", "sgmv_mx_medium.hip")]
+            "sgmv_mx_api.cpp", "sgmv_mx.hip", "sgmv_mx_large.hip", "sgmv_mx_medium.hip",
+            "sgmv_mx_skinny.hip")]
 
 STREAM_SOURCE = os.path.join(CSRC, "sgmv_stream.hip")
 STREAM_LIBRARY = os.path.join(HERE, "libsgmv_stream.so")

@@ -49,6 +49,7 @@ struct Plan {
   const void* kernel;
   int rows, cols, threads;
   int64_t row_tiles, col_tiles;
+  bool quantises = false;  // microscaled: the kernel takes the 16-bit inputs
 };
 
 int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
@@ -93,10 +94,41 @@ sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int 
   return tl < tm ? l : m;
 }
 
-sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan) {
+// The kernel for few rows of a microscaled call (x: its 16-bit inputs), or none.
+sgmv::TiledKernel mx_few(const sgmv::MatmulParams& p, const sgmv_matrix& x, int mode, int cus,
+                         bool* quantises) {
+  using namespace sgmv;
+  const TiledKernel m = mx_tiled_medium(x.dtype, mode);
+  const int64_t used = p.batches < p.T ? p.batches : p.T;
+  const bool adapted = p.num_slices > 0;
+  const bool fits = x.cols % 8 == 0 && aligned16(x.data) && x.row_stride % 8 == 0 &&
+                    (p.rows ? p.X : 256) * x.row_stride * 2 < int64_t(1) << 31;
+  *quantises = false;
+  if (p.grouped ? fits && tiles(p.T, p.batches) <= 16 && 2 * used * tiles(p.N, m.cols) <= cus
+                : fits && p.T <= 16) {
+    *quantises = true;
+    return mx_skinny_16(x.dtype, mode);
+  }
+  if (!p.grouped && p.T <= 32) return mx_skinny_32(x.dtype, adapted);
+  if (!p.grouped && p.T <= 64) return mx_skinny_64(x.dtype, adapted);
+  return TiledKernel{};
+}
+
+sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan,
+                      const sgmv_matrix* mx_inputs = nullptr) {
   using namespace sgmv;
   const int mode = gated ? 2 : p.grouped ? 1 : p.num_slices > 0 ? 3 : 0;
-  if (tiled_fits(p)) {
+  *plan = Plan{};
+  if (mx_inputs && tiled_fits(p)) {
+    int cus = 0;
+    const hipError_t e = device_compute_units(&cus);
+    if (e != hipSuccess)
+      return fail(SGMV_ERR_HIP, "device query failed: %s", hipGetErrorString(e));
+    bool quantises = false;
+    TiledKernel k = mx_few(p, *mx_inputs, mode, cus, &quantises);
+    if (!k.kernel) k = pick_tiled(p, wd, mode, cus);
+    *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0, quantises};
+  } else if (tiled_fits(p)) {
     int cus = 0;
     const hipError_t e = device_compute_units(&cus);
     if (e != hipSuccess)
@@ -123,7 +155,7 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
                           : p.T <= 32           ? matmul_skinny_32(wd, adapted)
                                                 : matmul_skinny_64_adapted(wd);
     const int64_t used = p.batches < p.T ? p.batches : p.T;
-    const bool few = p.ws ? false : p.grouped ? tiles(p.T, p.batches) <= 16 && 2 * used * tiles(p.N, m.cols) <= cus
+    const bool few = p.grouped ? tiles(p.T, p.batches) <= 16 && 2 * used * tiles(p.N, m.cols) <= cus
                                : p.T <= 16 || (p.T <= (adapted ? 64 : 32) &&
                                                f.rows * tiles(p.N, f.cols) <= (adapted ? 160 : 80) * (int64_t)cus);
     const TiledKernel k = few ? f : pick_tiled(p, wd, mode, cus);
@@ -295,6 +327,18 @@ void attach_mx(sgmv::MatmulParams& p, const sgmv_mx_stack& w, const Quantised& q
   p.ws_row_bytes = w.scale_stride;
   p.w_mat_bytes = w.rows * w.code_stride;
   p.H = (int32_t)(q.code_stride / 2);
+}
+
+// The inputs into the workspace, or handed to the kernel that quantises them.
+sgmv_status quantise_inputs(sgmv::MatmulParams& p, const Plan& plan, const sgmv_matrix& x,
+                            const Quantised& q, void* workspace, hipStream_t stream) {
+  if (!plan.quantises)
+    return sgmv::launch_mx_quantize(x, workspace, q.code_stride,
+                                    static_cast<char*>(workspace) + q.scales_at, q.scale_stride, stream);
+  p.x = x.data;
+  p.x_row_bytes = x.row_stride * 2;
+  p.mx_hidden = (int32_t)x.cols;
+  return SGMV_OK;
 }
 
 }  // namespace
@@ -517,10 +561,9 @@ sgmv_status sgmv_mx_lora_linear(sgmv_matrix inputs, sgmv_mx_stack weight, const 
     attach_adapters(p, slices, num_slices, K, L, b_seq_start_loc, seq_lens, lora_indices, batches,
                     static_cast<char*>(workspace) + q.bytes, down);
   Plan plan;
-  st = make_plan(p, x.dtype, false, &plan);
+  st = make_plan(p, x.dtype, false, &plan, &x);
   if (st != SGMV_OK) return st;
-  st = launch_mx_quantize(x, workspace, q.code_stride, static_cast<char*>(workspace) + q.scales_at,
-                          q.scale_stride, stream);
+  st = quantise_inputs(p, plan, x, q, workspace, stream);
   if (st != SGMV_OK) return st;
   if (p.num_slices > 0) {
     // The adapters' projections read the inputs themselves, not their 4-bit values.
@@ -593,11 +636,10 @@ sgmv_status sgmv_mx_grouped_gemm(sgmv_matrix inputs, sgmv_mx_stack weights, sgmv
   p.out_dtype = out.dtype;
   attach_mx(p, weights, q, workspace);
   Plan plan;
-  st = make_plan(p, x.dtype, gated != 0, &plan);
+  st = make_plan(p, x.dtype, gated != 0, &plan, &x);
   if (st != SGMV_OK) return st;
   if (x.rows > 0) {
-    st = launch_mx_quantize(x, workspace, q.code_stride, static_cast<char*>(workspace) + q.scales_at,
-                            q.scale_stride, stream);
+    st = quantise_inputs(p, plan, x, q, workspace, stream);
     if (st != SGMV_OK) return st;
   }
   return launch(plan, p, stream);

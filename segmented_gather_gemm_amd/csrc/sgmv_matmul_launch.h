@@ -58,6 +58,7 @@ struct MatmulParams {
   const void* ws;
   int64_t xs_row_bytes;
   int64_t ws_row_bytes;
+  int32_t mx_hidden;      // mx: values of an input row, where x has them in 16 bits
 };
 
 // Generic kernel: any size, stride and alignment (64 x 64 tiles).
@@ -80,5 +81,11 @@ TiledKernel mx_tiled_medium(int wd, int mode);
 TiledKernel matmul_skinny_16(int wd, int mode);
 TiledKernel matmul_skinny_32(int wd, bool adapted);
 TiledKernel matmul_skinny_64_adapted(int wd);
+// Microscaled weights, few rows: up to 16, whose 16-bit inputs the kernel
+// quantises (inputs of 16-byte aligned rows, hidden a multiple of eight), and
+// 32 or 64 of a dense call, quantised before.
+TiledKernel mx_skinny_16(int wd, int mode);
+TiledKernel mx_skinny_32(int wd, bool adapted);
+TiledKernel mx_skinny_64(int wd, bool adapted);
 
 }  // namespace sgmv
