@@ -50,6 +50,7 @@ struct Plan {
   int rows, cols, threads;
   int64_t row_tiles, col_tiles;
   bool quantises = false;  // microscaled: the kernel takes the 16-bit inputs
+  int strips = 0;          // microscaled, few rows: workgroups wanted
 };
 
 int64_t tiles(int64_t n, int64_t of) { return (n + of - 1) / of; }
@@ -94,24 +95,49 @@ sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int 
   return tl < tm ? l : m;
 }
 
-// The kernel for few rows of a microscaled call (x: its 16-bit inputs), or none.
+// The kernel for few rows of a microscaled call (x: its 16-bit inputs), or none;
+// *quantises: whether it does that with the inputs itself (16 rows).
+// Measured, us, few-row kernel and 128 x 128 tiles (which take a quantisation
+// of 3-4 besides), bfloat16, hidden 4096.  Dense: one row, 4096 and 28672
+// columns 6.8 and 12.5, 15.4 and 16.5; 16 rows 8.7 and 12.6, 17.7 and 16.1; 64 rows,
+// 4096, 8192 and 28672 columns 9.0 and 13.4, 12.6 and 13.8, 22.9 and 19.9.
+// Rank 16, 32 adapters, 6144 columns: 64 rows 12.7 and 36.9, 128 rows 18.8 and 52.4,
+// 256 rows 29.4 and 50.3; 4 adapters 14.0 and 19.0, 19.5 and 20.9, 30.6 and 18.6;
+// rank 64, 28672 columns 73 and 90, 131 and 112, 232 and 119.  Experts: 16 used
+// by a row each, hidden 2048, 2 x 1408 columns 14.5 and 14.9, 64 of 4 rows 46.9 and
+// 50.9, of 16 rows 66 and 54; hidden 14336, 4096 columns, 8 of one row 124 and 54
+// (the inputs are quantised again for every tile).
 sgmv::TiledKernel mx_few(const sgmv::MatmulParams& p, const sgmv_matrix& x, int mode, int cus,
                          bool* quantises) {
   using namespace sgmv;
-  const TiledKernel m = mx_tiled_medium(x.dtype, mode);
-  const int64_t used = p.batches < p.T ? p.batches : p.T;
-  const bool adapted = p.num_slices > 0;
   const bool fits = x.cols % 8 == 0 && aligned16(x.data) && x.row_stride % 8 == 0 &&
                     (p.rows ? p.X : 256) * x.row_stride * 2 < int64_t(1) << 31;
-  *quantises = false;
-  if (p.grouped ? fits && tiles(p.T, p.batches) <= 16 && 2 * used * tiles(p.N, m.cols) <= cus
-                : fits && p.T <= 16) {
-    *quantises = true;
-    return mx_skinny_16(x.dtype, mode);
+  const int64_t groups = p.H / 32;
+  *quantises = true;
+  if (p.grouped) {
+    // Few experts of a row or two, whose 128 x 128 tiles take one round.
+    const int64_t used = p.batches < p.T ? p.batches : p.T;
+    const int64_t medium = used * tiles(p.N, mx_tiled_medium(x.dtype, mode).cols);
+    if (fits && tiles(p.T, p.batches) <= 4 && medium <= 2 * cus && groups <= 64)
+      return mx_skinny(x.dtype, mode, 16, groups);
+    return TiledKernel{};
   }
-  if (!p.grouped && p.T <= 32) return mx_skinny_32(x.dtype, adapted);
-  if (!p.grouped && p.T <= 64) return mx_skinny_64(x.dtype, adapted);
-  return TiledKernel{};
+  if (fits && p.T <= 16) return mx_skinny(x.dtype, mode, 16, groups);
+  *quantises = false;
+  // Tiles of 16 columns a compute unit takes, with rows in 32s and in 64s.
+  const int64_t by32 = tiles(p.T, 32) * tiles(p.N, 16) / cus, by64 = tiles(p.T, 64) * tiles(p.N, 16) / cus;
+  bool few = p.T <= 32 || (p.T <= 64 && by64 <= 3);
+  if (p.num_slices > 0 && p.T <= 256) {
+    // A few-row workgroup's tile costs 2 us and 0.12 a rank; 128 x 128 tiles a
+    // round of 14 us and 3 for every 64 of their adapters' ranks (at least 8 each).
+    const int64_t row_tiles = tiles(p.T, 128), most = p.batches < p.T ? p.batches : p.T;
+    const int64_t near = tiles(most, row_tiles), seen = near < p.L ? near : p.L;  // adapters of a row tile
+    const int64_t rounds = tiles(seen * (p.K < 8 ? 8 : p.K), 64);
+    const int64_t launch = tiles(row_tiles * tiles(p.N, 128), 2 * cus);
+    few = 800 + by64 * (200 + 12 * p.K) <= launch * 1400 + rounds * 300;
+  }
+  if (!few) return TiledKernel{};
+  return mx_skinny(x.dtype, mode, p.T <= 32 || by32 <= 3 ? 32 : 64, groups);
 }
 
 sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* plan,
@@ -126,8 +152,10 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
       return fail(SGMV_ERR_HIP, "device query failed: %s", hipGetErrorString(e));
     bool quantises = false;
     TiledKernel k = mx_few(p, *mx_inputs, mode, cus, &quantises);
-    if (!k.kernel) k = pick_tiled(p, wd, mode, cus);
-    *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0, quantises};
+    const bool few = k.kernel != nullptr;
+    if (!few) k = pick_tiled(p, wd, mode, cus);
+    // Grouped: the row tiles below are a bound, about twice those there are.
+    *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0, few && quantises, !few ? 0 : p.grouped ? 2 * cus : cus};
   } else if (tiled_fits(p)) {
     int cus = 0;
     const hipError_t e = device_compute_units(&cus);
@@ -167,6 +195,13 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
   // Grouped: at most ceil(T / rows) + min(batches, T) row tiles.
   plan->row_tiles = tiles(p.T, plan->rows) + (p.grouped ? (p.batches < p.T ? p.batches : p.T) : 0);
   plan->col_tiles = tiles(p.N, plan->cols);
+  // The few-row kernel on microscaled weights walks over its column tiles: one
+  // workgroup a compute unit (two: 28672 columns and 16 rows 25.1 against 17.8
+  // us, one row 17.7 against 15.6), each with (nearly) as many of them.
+  if (plan->strips > 0) {
+    const int64_t strips = plan->strips / plan->row_tiles > 0 ? plan->strips / plan->row_tiles : 1;
+    plan->col_tiles = tiles(plan->col_tiles, tiles(plan->col_tiles, strips));
+  }
   // A launch holds fewer than 2^32 threads: refused here, ahead of the adapters'
   // own launch (64 x 64 tiles reach it at 2^36 results).
   if (plan->row_tiles * plan->col_tiles > (int64_t)UINT32_MAX / plan->threads)
@@ -338,6 +373,56 @@ sgmv_status quantise_inputs(sgmv::MatmulParams& p, const Plan& plan, const sgmv_
   p.x = x.data;
   p.x_row_bytes = x.row_stride * 2;
   p.mx_hidden = (int32_t)x.cols;
+  return SGMV_OK;
+}
+
+// Whether the adapters' projections of a call run token by token: for few rows
+// of inputs and lora_A rows (64 MiB of them with each token's read for itself).
+bool projects_by_token(const sgmv::MatmulParams& p, const sgmv_shrink_slice* down, const sgmv_matrix& x) {
+  if (x.cols % 8 != 0 || !aligned16(x.data) || x.row_stride % 8 != 0 || p.T > 64 ||
+      p.T * p.num_slices * p.K * x.cols * 2 > int64_t(64) << 20)
+    return false;
+  for (int i = 0; i < p.num_slices; ++i)
+    if (!aligned16(down[i].lora_a.data)) return false;
+  return true;
+}
+
+// Those projections and, unless the kernel does that itself, the inputs' codes and scales.
+sgmv_status project_by_token(sgmv::MatmulParams& p, const Plan& plan, const sgmv_shrink_slice* down,
+                             const sgmv_matrix& x, const Quantised& q, void* workspace, float scale,
+                             hipStream_t stream) {
+  using namespace sgmv;
+  MxProjectParams m{};
+  m.x = x.data;
+  m.x_row_bytes = x.row_stride * 2;
+  if (plan.quantises) {
+    quantise_inputs(p, plan, x, q, workspace, stream);
+  } else {
+    m.codes = workspace;
+    m.scales = static_cast<char*>(workspace) + q.scales_at;
+  }
+  m.code_stride = q.code_stride;
+  m.scale_stride = q.scale_stride;
+  m.start = p.start;
+  m.lens = p.lens;
+  m.idx = p.idx;
+  m.T = p.T;
+  m.H = (int32_t)x.cols;
+  m.K = p.K;
+  m.L = p.L;
+  m.batches = p.batches;
+  m.parts = (p.K + kMxProjectRows - 1) / kMxProjectRows;
+  m.v_stride = p.v_stride;
+  m.scale = scale;
+  for (int i = 0; i < p.num_slices; ++i) {
+    m.a[i] = down[i].lora_a.data;
+    m.v[i] = static_cast<float*>(down[i].out.data);
+  }
+  void* args[] = {&m};
+  const hipError_t e = hipLaunchKernel(mx_project_kernel(x.dtype),
+                                       dim3((unsigned)(m.parts * p.num_slices), (unsigned)p.T),
+                                       dim3(64 * kMxProjectWaves), args, 0, stream);
+  if (e != hipSuccess) return fail(SGMV_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   return SGMV_OK;
 }
 
@@ -563,6 +648,11 @@ sgmv_status sgmv_mx_lora_linear(sgmv_matrix inputs, sgmv_mx_stack weight, const 
   Plan plan;
   st = make_plan(p, x.dtype, false, &plan, &x);
   if (st != SGMV_OK) return st;
+  if (p.num_slices > 0 && projects_by_token(p, down, x)) {
+    st = project_by_token(p, plan, down, x, q, workspace, scale, stream);
+    if (st != SGMV_OK) return st;
+    return launch(plan, p, stream);
+  }
   st = quantise_inputs(p, plan, x, q, workspace, stream);
   if (st != SGMV_OK) return st;
   if (p.num_slices > 0) {

@@ -48,7 +48,7 @@ struct MatmulParams {
   int32_t out_dtype;
   int32_t add;            // dense: accumulate onto out
   int32_t vec_out;        // out's rows are 16-byte aligned and its columns a multiple of eight
-  int32_t col_tiles;      // column tiles of the launch
+  int32_t col_tiles;      // column tiles of the launch (mx_skinny: strips of them)
   int32_t row_tiles;      // dense: row tiles; grouped: bound on them (the device counts)
   int32_t num_slices;     // adapters: slices, rank, v's row stride (floats)
   int32_t K;
@@ -81,11 +81,11 @@ TiledKernel mx_tiled_medium(int wd, int mode);
 TiledKernel matmul_skinny_16(int wd, int mode);
 TiledKernel matmul_skinny_32(int wd, bool adapted);
 TiledKernel matmul_skinny_64_adapted(int wd);
-// Microscaled weights, few rows: up to 16, whose 16-bit inputs the kernel
-// quantises (inputs of 16-byte aligned rows, hidden a multiple of eight), and
-// 32 or 64 of a dense call, quantised before.
-TiledKernel mx_skinny_16(int wd, int mode);
-TiledKernel mx_skinny_32(int wd, bool adapted);
-TiledKernel mx_skinny_64(int wd, bool adapted);
+// Microscaled weights, few rows: 16 of a call or of a segment, whose 16-bit
+// inputs the kernel quantises (rows 16-byte aligned, hidden a multiple of
+// eight), and 32 or 64 of a dense call, quantised before.  A workgroup walks over tiles of 16 columns, col_tiles of
+// the launch apart.
+constexpr int kMxSkinnyWaves = 8;
+TiledKernel mx_skinny(int wd, int mode, int rows, int64_t groups);
 
 }  // namespace sgmv

@@ -26,19 +26,13 @@
 #pragma once
 
 #include "sgmv_matmul.h"
-#include "sgmv_mx.h"
 
 namespace sgmv {
 namespace dev {
 
 constexpr int kSkinnyWaves = 8;
 
-// Operands: 16-bit rows; microscaled rows whose inputs are 16-bit ones that the
-// kernel quantises (a lane's share of a row, for one matrix instruction, is a
-// whole block); microscaled rows on both sides.
-enum { kPlain = 0, kMxQuantise = 1, kMxBoth = 2 };
-
-template <int WD, int MODE, int MB, int NB, int G, int MX = kPlain>
+template <int WD, int MODE, int MB, int NB, int G>
 __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulParams p) {
   constexpr int kW = kSkinnyWaves, kNT = 64 * kW, ROWS = 16 * MB;
   constexpr int kMats = MODE == kGated ? 2 : 1;   // weight blocks per column block
@@ -54,10 +48,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
   const bool gather = (MODE == kGrouped || MODE == kGated) && p.rows != nullptr;
   const rsrc_t xr =
       uniform_rsrc(static_cast<const char*>(p.x) + (gather ? 0 : loc.row) * p.x_row_bytes,
-                   ((gather ? p.X : rows) - 1) * p.x_row_bytes +
-                       (int64_t)(MX == kMxQuantise ? p.mx_hidden : p.H) * 2);
+                   ((gather ? p.X : rows) - 1) * p.x_row_bytes + (int64_t)p.H * 2);
   uint32_t xoff[MB];
-  [[maybe_unused]] uint32_t xsoff[MB];
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
     const int r = m * 16 + lr;
@@ -68,7 +60,6 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
       ok = ok && src >= 0 && src < p.X;
     }
     xoff[m] = ok ? (uint32_t)(src * p.x_row_bytes) : kOut;
-    if constexpr (MX == kMxBoth) xsoff[m] = ok ? (uint32_t)(src * p.xs_row_bytes) : kOut;
   }
   rsrc_t wr[kMats];
 #pragma unroll
@@ -81,33 +72,12 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
   uint32_t woff[NB];
 #pragma unroll
   for (int n = 0; n < NB; ++n) woff[n] = (uint32_t)((n * 16 + lr) * p.w_row_bytes);
-  // The scales' rows.
-  [[maybe_unused]] rsrc_t xsr = xr, wsr[kMats];
-  [[maybe_unused]] uint32_t wsoff[NB];
-  if constexpr (MX != kPlain) {
-#pragma unroll
-    for (int g = 0; g < kMats; ++g) {
-      const int64_t nr = p.N - n0 < 16 * NB ? p.N - n0 : 16 * NB;
-      wsr[g] = uniform_rsrc(static_cast<const char*>(p.ws) +
-                                ((loc.e * (int64_t)kMats + g) * p.N + n0) * p.ws_row_bytes,
-                            (nr - 1) * p.ws_row_bytes + p.H / 8);
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) wsoff[n] = (uint32_t)((n * 16 + lr) * p.ws_row_bytes);
-  }
-  if constexpr (MX == kMxBoth)
-    xsr = uniform_rsrc(static_cast<const char*>(p.xs) + (gather ? 0 : loc.row) * p.xs_row_bytes,
-                       ((gather ? p.X : rows) - 1) * p.xs_row_bytes + p.H / 8);
 
   // Step u of this wave is step w + 8 u of the contraction: 64 elements, two
   // matrix instructions; lane quarter q holds blocks q and 4 + q of a row.
   const int steps = (p.H + 63) / 64;
   const int mine = (steps - wave + kW - 1) / kW;
-  // Microscaled: a step is two groups of 128 values, and a group's word of
-  // scales comes to all four quarters.
   u32x4 wv[G][kMats][NB][2], xv[G][MB][2];
-  [[maybe_unused]] u32x4 xraw[MX == kMxQuantise ? G : 1][MB][2][4];
-  [[maybe_unused]] uint32_t ws[G][kMats][NB][2], xs[G][MB][2];
   f32x4 acc[kMats][MB][NB] = {};
   auto load = [&](int g, int u) __attribute__((always_inline)) {
 #pragma unroll
@@ -119,34 +89,8 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
 #pragma unroll
         for (int n = 0; n < NB; ++n)
           buf_load8<WD>(wr[t], in ? woff[n] + k * 2u : kOut, &wv[g][t][n][s]);
-      if constexpr (MX != kPlain) {
-        const uint32_t word = ((wave + u * kW) * 2 + s) * 4u;
 #pragma unroll
-        for (int t = 0; t < kMats; ++t)
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-            ws[g][t][n][s] =
-                __builtin_amdgcn_raw_buffer_load_b32(wsr[t], (int)(in ? wsoff[n] + word : kOut), 0, 0);
-        if constexpr (MX == kMxBoth) {
-#pragma unroll
-          for (int m = 0; m < MB; ++m)
-            xs[g][m][s] =
-                __builtin_amdgcn_raw_buffer_load_b32(xsr, (int)(in ? xsoff[m] + word : kOut), 0, 0);
-        }
-      }
-      if constexpr (MX == kMxQuantise) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = k * 4 + i * 8;  // values: a word of codes holds four
-          const bool have = u < mine && at < p.mx_hidden;
-#pragma unroll
-          for (int m = 0; m < MB; ++m)
-            buf_load8<WD>(xr, have ? xoff[m] + at * 2u : kOut, &xraw[g][m][s][i]);
-        }
-      } else {
-#pragma unroll
-        for (int m = 0; m < MB; ++m) buf_load8<WD>(xr, in ? xoff[m] + k * 2u : kOut, &xv[g][m][s]);
-      }
+      for (int m = 0; m < MB; ++m) buf_load8<WD>(xr, in ? xoff[m] + k * 2u : kOut, &xv[g][m][s]);
     }
   };
   Segment seg{};
@@ -164,29 +108,14 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void matmul_skinny(MatmulPara
 #pragma unroll
     for (int g = 0; g < G; ++g) {  // past the last step: zeros
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if constexpr (MX == kMxQuantise) {
-#pragma unroll
-          for (int m = 0; m < MB; ++m) {
-            xs[g][m][s] = mx_scale(mx_largest<WD>(xraw[g][m][s]));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xv[g][m][s][i] = mx_codes8<WD>(&xraw[g][m][s][i], xs[g][m][s]);
-          }
-        }
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int t = 0; t < kMats; ++t)
 #pragma unroll
           for (int m = 0; m < MB; ++m)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-              if constexpr (MX == kPlain)
-                acc[t][m][n] = mfma<WD>(wv[g][t][n][s], xv[g][m][s], acc[t][m][n]);
-              else
-                acc[t][m][n] = mfma_fp4<0>(wv[g][t][n][s], xv[g][m][s], acc[t][m][n],
-                                           ws[g][t][n][s] >> (8 * lq),
-                                           xs[g][m][s] >> (MX == kMxBoth ? 8 * lq : 0));
-            }
-      }
+            for (int n = 0; n < NB; ++n)
+              acc[t][m][n] = mfma<WD>(wv[g][t][n][s], xv[g][m][s], acc[t][m][n]);
       load(g, u + G + g);
     }
   }

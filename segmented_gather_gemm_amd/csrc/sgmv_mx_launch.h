@@ -35,6 +35,33 @@ constexpr int64_t kMxMaxItems = int64_t(1) << 30;
 const void* mx_quantize_kernel(int xd);
 const void* mx_dequantize_kernel(int od);
 
+// Few tokens of a projection with adapters: the inputs' codes and scales (codes
+// null: none) and the adapters' projections v = scale * x . lora_a^T in one
+// launch.  A workgroup has one token and kMxProjectRows of a slice's rank.
+struct MxProjectParams {
+  const void* x;
+  void* codes;
+  void* scales;
+  const int64_t* start;
+  const int64_t* lens;
+  const int64_t* idx;
+  int64_t x_row_bytes;
+  int64_t code_stride;
+  int64_t scale_stride;
+  int64_t T;
+  int32_t H;               // a multiple of eight
+  int32_t K;
+  int32_t L;
+  int32_t batches;
+  int32_t parts;           // ceil(K / kMxProjectRows)
+  int32_t v_stride;
+  float scale;
+  const void* a[SGMV_MAX_SLICES];  // lora_A (L, K, H) contiguous, 16-byte aligned
+  float* v[SGMV_MAX_SLICES];       // (T, v_stride)
+};
+constexpr int kMxProjectWaves = 8, kMxProjectRows = 2 * kMxProjectWaves;
+const void* mx_project_kernel(int xd);
+
 // Quantise the rows of `x` into codes and scales (shapes checked by the caller).
 sgmv_status launch_mx_quantize(const sgmv_matrix& x, void* codes, int64_t code_stride, void* scales,
                                int64_t scale_stride, hipStream_t stream);
