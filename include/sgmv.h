@@ -537,7 +537,7 @@ typedef struct {
  * out           num * rows == inputs.rows, cols == hidden; must not overlap inputs.
  *
  * Returns SGMV_OK, or a status with nothing launched; SGMV_ERR_UNSUPPORTED
- * for more than 2^30 groups of 128 values.
+ * for more than 2^28 groups of 128 values.
  */
 sgmv_status sgmv_mx_quantize(sgmv_matrix inputs, sgmv_mx_stack out, hipStream_t stream);
 
@@ -587,7 +587,7 @@ sgmv_status sgmv_mx_dequantize(sgmv_mx_stack inputs, const int64_t* row_indices,
  * All else      as for sgmv_lora_linear.
  *
  * Returns what sgmv_lora_linear returns, and SGMV_ERR_UNSUPPORTED for inputs of
- * more than 2^30 groups of 128 values.
+ * more than 2^28 groups of 128 values.
  */
 sgmv_status sgmv_mx_lora_linear(sgmv_matrix inputs, sgmv_mx_stack weight, const void* bias,
                                 const sgmv_fused_slice* slices, int num_slices, sgmv_matrix out,
@@ -617,7 +617,7 @@ sgmv_status sgmv_mx_lora_linear_workspace_bytes(int64_t tokens, int64_t hidden, 
  * All else      as for sgmv_grouped_gemm.
  *
  * Returns what sgmv_grouped_gemm returns, and SGMV_ERR_UNSUPPORTED for inputs
- * of more than 2^30 groups of 128 values.
+ * of more than 2^28 groups of 128 values.
  */
 sgmv_status sgmv_mx_grouped_gemm(sgmv_matrix inputs, sgmv_mx_stack weights, sgmv_matrix out,
                                  const int64_t* row_indices, const int64_t* b_seq_start_loc,

@@ -178,6 +178,7 @@ _DTYPE_CODES = {_torch.float16: 0, _torch.bfloat16: 1, _torch.float32: 2}
 # The current stream's raw handle without building a Stream object (a
 # measurable part of a call's host time); the public route where absent.
 _RAW_STREAM = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+_CURRENT_DEVICE = getattr(_torch._C, "_cuda_getDevice", _torch.cuda.current_device)
 
 
 def _stream(device) -> int:
@@ -188,7 +189,7 @@ def _stream(device) -> int:
 
 def _call_on(device, fn, *args):
     """fn(*args) with `device` current (made current only when it is not)."""
-    if _torch.cuda.current_device() == device.index:
+    if _CURRENT_DEVICE() == device.index:
         return fn(*args)
     with _torch.cuda.device(device):
         return fn(*args)
@@ -690,23 +691,50 @@ def mx_row_bytes(hidden: int) -> Tuple[int, int]:
     return 64 * groups, 4 * groups
 
 
+def _mx_rows(t, what: str, device, dims: int, need: int):
+    """(matrices, rows, bytes from row to row) of codes or scales, `need` bytes a row."""
+    shape = t.shape
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}")
+    if len(shape) != dims or shape[-1] != need or t.dtype is not _torch.uint8:
+        raise ValueError(f"{what} must be {dims}-D uint8 with {need} bytes a row, got {tuple(shape)} "
+                         f"{t.dtype}")
+    if dims == 3:
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must have contiguous matrices")
+        return shape[0], shape[1], need
+    stride, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    return 1, shape[0], stride if shape[0] > 1 else need
+
+
 def _mx_stack(codes, scales, hidden: int, what: str, device, dims: int) -> MxStack:
     """codes and scales, (rows, bytes) or (matrices, rows, bytes) of uint8, as
     rows of `hidden` values."""
-    for t, n, need in zip((codes, scales), ("codes", "scales"), mx_row_bytes(hidden)):
-        if t.device != device:
-            raise ValueError(f"{what} {n} must be on {device}")
-        if t.dtype != _torch.uint8 or t.dim() != dims or t.shape[-1] != need:
-            raise ValueError(f"{what} {n} must be {dims}-D uint8 with {need} bytes a row of {hidden} "
-                             f"values, got {tuple(t.shape)} {t.dtype}")
-        if t.shape[-1] > 1 and t.stride(-1) != 1 or (dims == 3 and not t.is_contiguous()):
-            raise ValueError(f"{what} {n} must have contiguous " + ("matrices" if dims == 3 else "rows"))
-    if codes.shape[:-1] != scales.shape[:-1]:
+    groups = (hidden + 127) // 128
+    num, rows, code_stride = _mx_rows(codes, what + " codes", device, dims, 64 * groups)
+    num2, rows2, scale_stride = _mx_rows(scales, what + " scales", device, dims, 4 * groups)
+    if rows != rows2 or num != num2:
         raise ValueError(f"{what}: codes {tuple(codes.shape)} and scales {tuple(scales.shape)} differ "
                          "in rows")
-    strides = [t.stride(-2) if t.shape[-2] > 1 or dims == 3 else t.shape[-1] for t in (codes, scales)]
-    return MxStack(codes.data_ptr(), scales.data_ptr(), codes.shape[0] if dims == 3 else 1,
-                   codes.shape[-2], int(hidden), *strides)
+    return MxStack(codes.data_ptr(), scales.data_ptr(), num, rows, hidden, code_stride, scale_stride)
+
+
+def _row_indices(t, rows: int, device):
+    if t is None:
+        return None
+    t = _meta(t, "row_indices_tensor", device)
+    if t.shape[0] < rows:
+        raise ValueError("row_indices_tensor shorter than the number of output rows")
+    return t
+
+
+def _gpu(t, what: str):
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"{what} must be a GPU tensor")
+    return device
 
 
 def sgmv_mx_quantize(inputs, codes, scales):
@@ -717,7 +745,7 @@ def sgmv_mx_quantize(inputs, codes, scales):
     nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 of it (ties to the even code, the even
     value in a byte's low half); 255 marks a block with an infinity or NaN.
     Enqueued on the current stream."""
-    device, _ = _common(inputs, ())
+    device = _gpu(inputs, "inputs")
     x = _matrix(inputs, "inputs")
     q = _mx_stack(codes, scales, x.cols, "output", device, 2)
     rc = _call_on(device, lib.sgmv_mx_quantize, x, q, _stream(device))
@@ -730,17 +758,21 @@ def sgmv_mx_dequantize(codes, scales, output_tensor, row_indices_tensor=None):
     """output_tensor[t] = the values of row row_indices_tensor[t] (None: row t)
     of codes and scales; indices outside their rows give rows of zeros.
     Enqueued on the current stream."""
-    device, kept = _common(output_tensor, () if row_indices_tensor is None else
-                           [(row_indices_tensor, "row_indices_tensor")])
+    device = _gpu(output_tensor, "output_tensor")
     out = _matrix(output_tensor, "output_tensor")
-    if kept and kept[0].shape[0] < out.rows:
-        raise ValueError("row_indices_tensor shorter than the number of output rows")
+    rows = _row_indices(row_indices_tensor, out.rows, device)
     q = _mx_stack(codes, scales, out.cols, "input", device, 2)
-    rc = _call_on(device, lib.sgmv_mx_dequantize, q, kept[0].data_ptr() if kept else None, out,
+    rc = _call_on(device, lib.sgmv_mx_dequantize, q, None if rows is None else rows.data_ptr(), out,
                   _stream(device))
     if rc != SGMV_OK:
         _raise(rc)
     return output_tensor
+
+
+def _mx_bytes(rows: int, hidden: int) -> int:
+    """The quantised inputs' part of a workspace (as the library sizes it)."""
+    groups = (hidden + 127) // 128
+    return -(-rows * 64 * groups // 256) * 256 + -(-rows * 4 * groups // 256) * 256
 
 
 def mx_lora_linear_workspace_bytes(tokens: int, hidden: int, num_slices: int = 0, rank: int = 0) -> int:
@@ -767,9 +799,10 @@ def sgmv_mx_lora_linear(inputs, weight_codes, weight_scales, slices: Sequence[Tu
     the call)."""
     if len(slices) > MAX_SLICES:
         raise ValueError(f"at most {MAX_SLICES} slices, got {len(slices)}")
-    device, (start, lens, idx) = _common(output_tensor, [
-        (b_seq_start_loc, "b_seq_start_loc"), (seq_len_tensor, "seq_len_tensor"),
-        (lora_indices_tensor, "lora_indices_tensor")])
+    device = _gpu(output_tensor, "output_tensor")
+    start = _meta(b_seq_start_loc, "b_seq_start_loc", device)
+    lens = _meta(seq_len_tensor, "seq_len_tensor", device)
+    idx = _meta(lora_indices_tensor, "lora_indices_tensor", device)
     if inputs.device != device:
         raise ValueError(f"inputs must be on {device}")
     if start.shape[0] < batches or lens.shape[0] < batches or idx.shape[0] < batches:
@@ -781,9 +814,9 @@ def sgmv_mx_lora_linear(inputs, weight_codes, weight_scales, slices: Sequence[Tu
     arr = _fused_slices(slices, device)
     need = 0
     if workspace is None:
-        adapted = slices and batches > 0
-        need = mx_lora_linear_workspace_bytes(x.rows, x.cols, len(slices) if adapted else 0,
-                                              arr[0].lora_a.rows if adapted else 0)
+        need = _mx_bytes(x.rows, x.cols)
+        if slices and batches > 0:
+            need += len(slices) * (-(-x.rows * -(-arr[0].lora_a.rows // 8) * 32 // 256) * 256)
     keep, ws, ws_bytes = _scratch(device, workspace, need)
     rc = _call_on(device, lib.sgmv_mx_lora_linear, x, w, bias_ptr, arr, len(slices), out,
                   start.data_ptr(), lens.data_ptr(), idx.data_ptr(), int(batches),
@@ -802,27 +835,25 @@ def sgmv_mx_grouped_gemm(inputs, expert_codes, expert_scales, output_tensor, b_s
     quantised within the call.  Enqueued on the current stream.  `workspace`:
     a uint8 tensor of mx_grouped_gemm_workspace_bytes(), or None (taken from
     torch's allocator for the call)."""
-    metas = [(b_seq_start_loc, "b_seq_start_loc"), (seq_len_tensor, "seq_len_tensor")]
-    if expert_indices_tensor is not None:
-        metas.append((expert_indices_tensor, "expert_indices_tensor"))
-    device, kept = _common(output_tensor, metas)
-    if any(m.shape[0] < batches for m in kept):
+    device = _gpu(output_tensor, "output_tensor")
+    start = _meta(b_seq_start_loc, "b_seq_start_loc", device)
+    lens = _meta(seq_len_tensor, "seq_len_tensor", device)
+    idx = None if expert_indices_tensor is None else \
+        _meta(expert_indices_tensor, "expert_indices_tensor", device)
+    if start.shape[0] < batches or lens.shape[0] < batches or \
+            (idx is not None and idx.shape[0] < batches):
         raise ValueError("segment metadata shorter than batches")
     if inputs.device != device:
         raise ValueError(f"inputs must be on {device}")
     x = _matrix(inputs, "inputs")
     w = _mx_stack(expert_codes, expert_scales, x.cols, "expert", device, 3)
     out = _matrix(output_tensor, "output_tensor")
-    rows = None
-    if row_indices_tensor is not None:
-        rows = _meta(row_indices_tensor, "row_indices_tensor", device)
-        if rows.shape[0] < out.rows:
-            raise ValueError("row_indices_tensor shorter than the number of output rows")
-    need = mx_grouped_gemm_workspace_bytes(x.rows, x.cols) if workspace is None else 0
+    rows = _row_indices(row_indices_tensor, out.rows, device)
+    need = _mx_bytes(x.rows, x.cols) if workspace is None else 0
     keep, ws, ws_bytes = _scratch(device, workspace, need)
     rc = _call_on(device, lib.sgmv_mx_grouped_gemm, x, w, out,
-                  None if rows is None else rows.data_ptr(), kept[0].data_ptr(),
-                  kept[1].data_ptr(), kept[2].data_ptr() if len(kept) > 2 else None, int(batches),
+                  None if rows is None else rows.data_ptr(), start.data_ptr(), lens.data_ptr(),
+                  None if idx is None else idx.data_ptr(), int(batches),
                   int(max_seq_length), int(bool(gated)), ws, ws_bytes, _stream(device))
     if rc != SGMV_OK:
         _raise(rc)

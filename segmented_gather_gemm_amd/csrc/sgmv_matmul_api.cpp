@@ -115,10 +115,9 @@ sgmv::TiledKernel mx_few(const sgmv::MatmulParams& p, const sgmv_matrix& x, int 
   const int64_t groups = p.H / 32;
   *quantises = true;
   if (p.grouped) {
-    // Few experts of a row or two, whose 128 x 128 tiles take one round.
+    // Few experts of up to 16 rows: 128 x 128 tiles read more experts' weights faster.
     const int64_t used = p.batches < p.T ? p.batches : p.T;
-    const int64_t medium = used * tiles(p.N, mx_tiled_medium(x.dtype, mode).cols);
-    if (fits && tiles(p.T, p.batches) <= 4 && medium <= 2 * cus && groups <= 64)
+    if (fits && tiles(p.T, p.batches) <= 16 && used * tiles(p.N, 16) <= 6 * cus && groups <= 64)
       return mx_skinny(x.dtype, mode, 16, groups);
     return TiledKernel{};
   }
@@ -345,7 +344,7 @@ sgmv_status check_quantised(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1)
     return fail(SGMV_ERR_INVALID_ARGUMENT, "rows must be >= 0 and hidden >= 1");
   if (cols > INT32_MAX - 4096 || rows > sgmv::kMxMaxItems / sgmv::limits::mx_groups(cols))
-    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^30 groups of 128 inputs");
+    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^28 groups of 128 inputs");
   return SGMV_OK;
 }
 

@@ -179,9 +179,13 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // would move operands between the two right ahead of their use.
   constexpr bool kAcc = !MX || S::kOccupancy == 1;
   __shared__ uint16_t a00[HM * 64], a01[HM * 64], a10[HM * 64], a11[HM * 64];
-  __shared__ uint16_t b00[HN * 64], b01[HN * 64], b10[HN * 64], b11[HN * 64];
+  // b01 goes on with the staged scales (input rows, then weight rows; 16 bytes each): the
+  // compiler makes reads of LDS wait for the loads into the same array that are
+  // on their way, or for all loads if there are none, and when scales are read
+  // those of b01 have long arrived.
+  constexpr int kScales = MX ? (S::BM + S::BN) * 8 : 0;
+  __shared__ uint16_t b00[HN * 64], b01[HN * 64 + kScales], b10[HN * 64], b11[HN * 64];
   __shared__ int32_t sh[S::kWaves + 4];
-  __shared__ u32x4 scales[MX ? S::BM + S::BN : 1];  // input rows, then weight rows
 
   const TileLoc loc = find_tile<S::kNT>(p, S::BM, sh);
   if (loc.row < 0) return;
@@ -273,17 +277,17 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   // resource's end (a half of the weights may have no row at all).
   // MX: a load's rows lie a wave-uniform distance from those of the lane's
   // first, whose offset alone takes a register (rows that follow each other
-  // and pass the tile's end pass the resource's); the distance is worked out
-  // anew each time, or the compiler keeps the sums.
+  // and pass the tile's end pass the resource's); the sum is made anew each
+  // time, or the compiler keeps all of them.
   auto here = [](int64_t v) __attribute__((always_inline)) {
-    int32_t bytes = (int32_t)v;
+    uint32_t bytes = (uint32_t)v;
     asm volatile("" : "+s"(bytes));
     return bytes;
   };
   auto load_a = [&](uint16_t* dst, int h, int t, int i) __attribute__((always_inline)) {
     const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
     const uint32_t row = MX && (MODE == kDense || MODE == kAdapted)
-                             ? xoff[0][0] + (uint32_t)((h * HM + i * 8) * here(p.x_row_bytes))
+                             ? xoff[0][0] + here((h * HM + i * 8) * p.x_row_bytes)
                              : xoff[h][i];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(dst + (wave * LL + i) * 512), 16,
                                              (int)(in ? row + (uint32_t)t * 128u : kOut), 0,
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     const bool in = t * 64 + 64 <= p.H || t * 64 + chunk * 8 < p.H;
     static_assert(16 * FN % (8 * LL) == 0, "a wave's loads of a half stay within a block of rows");
     const uint32_t row =
-        MX ? woff[0] + (uint32_t)((i / 2 * 4 + i % 2 * 8 * FN) * here(p.w_row_bytes)) : woff[i];
+        MX ? woff[0] + here((i / 2 * 4 + i % 2 * 8 * FN) * p.w_row_bytes) : woff[i];
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[h], (lds_void*)(dst + (wave * LL + i) * 512), 16,
                                              (int)(in ? row + (uint32_t)t * 128u : kOut), 0, 0,
                                              0);
@@ -304,8 +308,13 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   const int orow = lane & 15, oq = lane >> 4;
   u32x4 xa[3][2 * FM], wb[3][2 * FN];   // three sets of a part's operands
   f32x4 acc[2][2][FM][FN] = {};         // [A half][B half]
+  // MX: the lane's offsets within a block, of both parts and in the scales;
+  // asm statements in each step keep the compiler from holding their sums with
+  // each array's address (34 registers).
+  int off[3] = {orow * 64 + (oq ^ (orow & 7)) * 8, orow * 64 + ((oq + 4) ^ (orow & 7)) * 8, orow * 8 + oq * 2};
   auto operand = [&](const uint16_t* src, int block, int s) __attribute__((always_inline)) {
-    return operand_of(src, block, s, orow, oq);
+    if constexpr (MX) return *reinterpret_cast<const u32x4*>(src + block * 1024 + off[s]);
+    else return operand_of(src, block, s, orow, oq);
   };
   // Operand i of part s into set `to`: the 2 FN of B, then the 2 FM of A.
   auto read_one = [&](const uint16_t* A0, const uint16_t* A1, const uint16_t* B0,
@@ -332,8 +341,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
   constexpr int kEarly = S::kOccupancy == 1                    ? kLoads * 5 / 8
                          : MODE == kDense || MODE == kAdapted ? kLoads
                                                               : kLoads * 3 / 4;
-  // MX: scales come for two steps (four groups) at a time.  They are loaded
-  // during the first of the two steps before theirs, go to LDS in the second,
+  // MX: scales come for two steps (four groups) at a time.  They are loaded at
+  // the start of part 0 of the step before theirs, where a set of operand
+  // registers is free, and go to LDS at its end (a line of them serves eight
+  // times, so that most come from the L2),
   // a row's four words transposed, so that a lane reads its four groups'
   // scales as one word, and from there into the registers of those they
   // follow, each after its last use.  Words past the row's end, which may be
@@ -351,16 +362,16 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
     for (int j = 0; j < kS; ++j) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) sraw[j][w] &= 32 * (2 * t + w) < p.H ? ~0u : 0u;
-      scales[threadIdx.x + j * S::kNT] = transpose_bytes(sraw[j]);
+      *reinterpret_cast<u32x4*>(b01 + HN * 64 + (threadIdx.x + j * S::kNT) * 8) = transpose_bytes(sraw[j]);
     }
   };
   auto read_sa = [&](int m) __attribute__((always_inline)) {
-    const int r = (m / FM) * HM + (wm * FM + m % FM) * 16 + orow;
-    sa[m] = reinterpret_cast<const uint32_t*>(scales + r)[oq];
+    const int r = (m / FM) * HM + (wm * FM + m % FM) * 16;
+    sa[m] = *reinterpret_cast<const uint32_t*>(b01 + HN * 64 + r * 8 + off[2]);
   };
   auto read_sb = [&](int n) __attribute__((always_inline)) {
-    const int r = S::BM + (n / FN) * HN + (wn * FN + n % FN) * 16 + orow;
-    sb[n] = reinterpret_cast<const uint32_t*>(scales + r)[oq];
+    const int r = S::BM + (n / FN) * HN + (wn * FN + n % FN) * 16;
+    sb[n] = *reinterpret_cast<const uint32_t*>(b01 + HN * 64 + r * 8 + off[2]);
   };
   // Step t, whose operands are in sets 0 and 1 + t % 2, with its LDS
   // (A0, A1, B0, B1) free and the next step's in (C0, C1, D0, D1).  BOTH:
@@ -395,6 +406,10 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
       }
     };
     int loads = 0, reads = 0;
+    if constexpr (MX && kSet == 2) {
+      load_scales(t + 1);
+      pin();
+    }
     rows_of(std::integral_constant<int, 0>{}, 0, [&](int k) __attribute__((always_inline)) {
       if (loads * kMfma <= k * kEarly && loads < kEarly) {
         pin();
@@ -402,18 +417,13 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
         pin();
       }
     });
-    if constexpr (MX && kSet == 1) {
-      pin();
-      load_scales(t + 2);
-      wait_loads<kEarly + kS>();
-    } else {
-      wait_loads<kEarly>();
-    }
+    wait_loads<kEarly>();
     if constexpr (MX && kSet == 2) {
       store_scales(t + 1);
       wait_lds_reads();
     }
     wg_barrier();
+    if constexpr (MX) asm volatile("" : "+v"(off[0]), "+v"(off[1]), "+v"(off[2]));
     rows_of(std::integral_constant<int, 1>{}, kSet, [&](int k) __attribute__((always_inline)) {
       if ((loads - kEarly) * kMfma <= k * (kLoads - kEarly) && loads < kLoads) {
         pin();

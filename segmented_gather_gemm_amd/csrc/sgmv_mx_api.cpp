@@ -41,7 +41,7 @@ sgmv_status check_values(const sgmv_matrix& m, const char* what) {
     return fail(SGMV_ERR_INVALID_ARGUMENT, "%s shape (%lld, %lld) with row stride %lld is invalid",
                 what, (long long)m.rows, (long long)m.cols, (long long)m.row_stride);
   if (m.cols > INT32_MAX - 4096 || m.rows > kMxMaxItems / limits::mx_groups(m.cols))
-    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^30 groups of 128 values");
+    return fail(SGMV_ERR_UNSUPPORTED, "more than 2^28 groups of 128 values");
   return SGMV_OK;
 }
 

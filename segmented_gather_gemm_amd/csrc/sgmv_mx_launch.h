@@ -29,9 +29,9 @@ struct MxParams {
 };
 
 constexpr int kMxThreads = 256;
-constexpr int kMxUnroll = 4;                              // groups a lane works on
+constexpr int kMxUnroll = 2;                              // groups a lane works on
 constexpr int kMxItems = kMxThreads / 16 * kMxUnroll;     // groups of a workgroup
-constexpr int64_t kMxMaxItems = int64_t(1) << 30;
+constexpr int64_t kMxMaxItems = int64_t(1) << 28;         // a launch holds fewer than 2^32 threads
 const void* mx_quantize_kernel(int xd);
 const void* mx_dequantize_kernel(int od);
 

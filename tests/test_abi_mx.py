@@ -54,7 +54,7 @@ def test_quantize_rejects_outputs(kw, status, frag):
 
 @pytest.mark.parametrize("kw,status,frag", [
     (dict(dt=5), INVALID, "dtype"), (dict(stride=199), INVALID, "row stride"), (dict(rows=-1), INVALID, "shape"),
-    (dict(cols=0), INVALID, "shape"), (dict(data=0), INVALID, "null"), (dict(rows=1 << 30), UNSUPPORTED, "2^30")])
+    (dict(cols=0), INVALID, "shape"), (dict(data=0), INVALID, "null"), (dict(rows=1 << 30), UNSUPPORTED, "2^28")])
 def test_quantize_rejects_inputs(kw, status, frag):
     assert sg.lib.sgmv_mx_quantize(x_(**kw), mx(), None) == status and frag in error()
 
@@ -66,7 +66,7 @@ def test_dequantize_rejects_inputs(kw, status, frag):
 
 @pytest.mark.parametrize("kw,status,frag", [
     (dict(dt=5), INVALID, "dtype"), (dict(stride=199), INVALID, "row stride"), (dict(data=0), INVALID, "null"),
-    (dict(rows=1 << 30), UNSUPPORTED, "2^30")])
+    (dict(rows=1 << 30), UNSUPPORTED, "2^28")])
 def test_dequantize_rejects_outputs(kw, status, frag):
     assert sg.lib.sgmv_mx_dequantize(mx(), FAKE, x_(**kw), None) == status and frag in error()
 
@@ -154,6 +154,11 @@ def test_workspace_sizes():
     assert sg.mx_grouped_gemm_workspace_bytes(0, 200) == 0
     assert sg.mx_lora_linear_workspace_bytes(10, 200) == 1536
     assert sg.mx_lora_linear_workspace_bytes(10, 200, 2, 8) == 1536 + sg.lora_linear_workspace_bytes(10, 2, 8)
+    # what the wrappers take when no workspace is given
+    for rows, hidden, slices, rank in ((1, 1, 0, 0), (10, 200, 2, 8), (77, 4104, 3, 13), (0, 64, 1, 16), (2501, 2056, 1, 24)):
+        assert sg._mx_bytes(rows, hidden) == sg.mx_grouped_gemm_workspace_bytes(rows, hidden)
+        assert sg.mx_lora_linear_workspace_bytes(rows, hidden, slices, rank) - sg._mx_bytes(rows, hidden) == \
+            slices * (-(-rows * -(-rank // 8) * 32 // 256) * 256) == sg.lora_linear_workspace_bytes(rows, slices, rank)
     for bad in ((-1, 8), (1, 0)):
         with pytest.raises(ValueError):
             sg.mx_grouped_gemm_workspace_bytes(*bad)
