@@ -82,9 +82,8 @@ bool tiled_fits(const sgmv::MatmulParams& p) {
 // are near each other (32 experts x 188 rows of the same, 124 and 121 us) it
 // may miss by 5%.  A segment fills half of its last tile on average.
 sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int cus) {
-  const bool mx = p.ws != nullptr;
-  const sgmv::TiledKernel l = mx ? sgmv::mx_tiled_large(wd, mode) : sgmv::matmul_tiled_large(wd, mode);
-  const sgmv::TiledKernel m = mx ? sgmv::mx_tiled_medium(wd, mode) : sgmv::matmul_tiled_medium(wd, mode);
+  const sgmv::TiledKernel l = sgmv::matmul_tiled_large(wd, mode);
+  const sgmv::TiledKernel m = sgmv::matmul_tiled_medium(wd, mode);
   auto count = [&](const sgmv::TiledKernel& k) {
     const int64_t rows = p.grouped ? (2 * p.T + p.batches * k.rows) / (2 * k.rows) : tiles(p.T, k.rows);
     return rows * tiles(p.N, k.cols);
@@ -92,6 +91,33 @@ sgmv::TiledKernel pick_tiled(const sgmv::MatmulParams& p, int wd, int mode, int 
   const int64_t nl = count(l), nm = count(m);
   const int64_t tl = 100 * tiles(nl, cus);
   const int64_t tm = nm <= cus ? 34 : nm <= 4 * cus ? 57 * tiles(nm, 2 * cus) : 75 * nm / (2 * cus);
+  return tl < tm ? l : m;
+}
+
+// The same for microscaled operands, in tenths of a microsecond, by the steps
+// of 256 along the contraction: a round of large tiles takes 13 us and 1.84 a
+// step (6 and 1.6 with few of them), medium ones 6 and 0.75 a step with one workgroup
+// per compute unit, else 3.5 and for each round of two 4.5 and 1.25 a step (1.35
+// where many rounds bind at the L2); adapters add 13 and 5.5 us a round.  Measured,
+// large and medium, us, 4096 columns: hidden 2048, 512, 2048 and 4096 rows 21 and
+// 11, 24 and 17, 28 and 30; hidden 4096, 512, 2048 and 4096 rows 32 and 16, 36 and 28,
+// 43 and 49; hidden 8192, 2048 rows 60 and 46; 2048 rows with 16 adapters 49 and 33;
+// 2501 rows, hidden 2056, 5000 columns, float32 results 55 and 48; 64 experts of
+// 94 rows 83 and 69; 8 of 128 rows, hidden 4096, 2 x 14336 columns 165 and 172.
+sgmv::TiledKernel pick_mx_tiled(const sgmv::MatmulParams& p, int wd, int mode, int cus) {
+  const sgmv::TiledKernel l = sgmv::mx_tiled_large(wd, mode);
+  const sgmv::TiledKernel m = sgmv::mx_tiled_medium(wd, mode);
+  auto count = [&](const sgmv::TiledKernel& k) {
+    const int64_t rows = p.grouped ? (2 * p.T + p.batches * k.rows) / (2 * k.rows) : tiles(p.T, k.rows);
+    return (double)(rows > 0 ? rows : 1) * tiles(p.N, k.cols) / cus;
+  };
+  const double steps = tiles(p.H, 64), nl = count(l), nm = count(m) / 2;
+  const double full = (double)(int64_t)nl, part = nl - full;
+  const double adapted = p.num_slices > 0 ? 1 : 0;
+  const double tl = full * (130 + 18.4 * steps + 130 * adapted) +
+                    (part > 0 ? 60 + 16 * steps + part * (70 + 2.4 * steps + 130 * adapted) : 0);
+  const double tm = nm <= 0.5 ? 60 + 7.5 * steps + 55 * adapted
+                              : 35 + (nm < 1 ? 1 : nm) * (45 + (nm > 4 ? 13.5 : 12.5) * steps + 55 * adapted);
   return tl < tm ? l : m;
 }
 
@@ -152,7 +178,7 @@ sgmv_status make_plan(const sgmv::MatmulParams& p, int wd, bool gated, Plan* pla
     bool quantises = false;
     TiledKernel k = mx_few(p, *mx_inputs, mode, cus, &quantises);
     const bool few = k.kernel != nullptr;
-    if (!few) k = pick_tiled(p, wd, mode, cus);
+    if (!few) k = pick_mx_tiled(p, wd, mode, cus);
     // Grouped: the row tiles below are a bound, about twice those there are.
     *plan = Plan{k.kernel, k.rows, k.cols, k.threads, 0, 0, few && quantises, !few ? 0 : p.grouped ? 2 * cus : cus};
   } else if (tiled_fits(p)) {
