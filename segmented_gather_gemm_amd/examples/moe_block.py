@@ -5,12 +5,13 @@ experts on the normalised result.
 
     python segmented_gather_gemm_amd/examples/moe_block.py
 
-Random weights; the result is compared with the same block in plain torch
-operations in 64 bits.
+Random weights, in 16 bits and (four_bit) with the projection and the experts
+in microscaled 4-bit form; the result is compared with the same block in plain
+torch operations in 64 bits.
 """
 import os
 import sys
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
@@ -39,19 +40,54 @@ def random_weights(hidden, width, experts, adapters, rank, seed=0, device="cuda"
                    normal(experts, 2 * width, hidden, sigma=hidden ** -0.5), normal(experts, hidden, width, sigma=width ** -0.5))
 
 
+def packed(w):
+    """A weight (rows, hidden), or a stack of them, as microscaled 4-bit codes and scales."""
+    rows = w.view(-1, w.shape[-1])
+    codes, scales = (torch.empty(rows.shape[0], n, dtype=torch.uint8, device=w.device) for n in sg.mx_row_bytes(w.shape[-1]))
+    sg.sgmv_mx_quantize(rows, codes, scales)
+    return codes.view(*w.shape[:-1], -1), scales.view(*w.shape[:-1], -1)
+
+
+def unpacked(pair, like):
+    """The 16-bit weight, of the shape and dtype of `like`, that codes and scales stand for."""
+    codes, scales = pair
+    out = torch.empty_like(like)
+    sg.sgmv_mx_dequantize(codes.view(-1, codes.shape[-1]), scales.view(-1, scales.shape[-1]), out.view(-1, out.shape[-1]))
+    return out
+
+
+def four_bit(w):
+    """The same weights, those of the projection and of the experts as (codes, scales) pairs."""
+    return replace(w, proj=packed(w.proj), gate_up=packed(w.gate_up), down=packed(w.down))
+
+
+def project(x, weight, *rest, **options):
+    if isinstance(weight, tuple):
+        return sg.sgmv_mx_lora_linear(x, *weight, *rest, **options)
+    return sg.sgmv_lora_linear(x, weight, *rest, **options)
+
+
+def experts(x, weights, *rest, **options):
+    if isinstance(weights, tuple):
+        return sg.sgmv_mx_grouped_gemm(x, *weights, *rest, **options)
+    return sg.sgmv_grouped_gemm(x, weights, *rest, **options)
+
+
 def norm(x):
     return (x.float() * torch.rsqrt(x.float().square().mean(dim=1, keepdim=True) + 1e-6)).to(x.dtype)
 
 
-def block(w, attn, residual, start, lens, adapter, top_k, scale=2.0):
+def block(w, attn, residual, start, lens, adapter, top_k, scale=2.0, seen=None):
     """residual (tokens, hidden) is updated in place; attn holds the tokens' attention outputs, packed
-    by request (start, lens), adapter the requests' adapters (-1: none)."""
+    by request (start, lens), adapter the requests' adapters (-1: none).  `seen` takes the tensors
+    between the steps."""
     T, H = residual.shape
     E, k, dev = w.router.shape[0], top_k, residual.device
     requests, longest = lens.shape[0], T
     # x = residual + proj attn + the requests' adapters, in one rounding
-    sg.sgmv_lora_linear(attn, w.proj, [(w.lora_a, w.lora_b, 0)], residual, start, lens, adapter, requests,
-                        longest, scaling=scale, add_inputs=True)
+    project(attn, w.proj, [(w.lora_a, w.lora_b, 0)], residual, start, lens, adapter, requests, longest,
+            scaling=scale, add_inputs=True)
+    projected = residual.clone() if seen is not None else None
     x = norm(residual)
     # choices of experts, and the choices' rows in the order of the experts
     logits = torch.empty(T, E, dtype=torch.float32, device=dev)
@@ -61,11 +97,15 @@ def block(w, attn, residual, start, lens, adapter, top_k, scale=2.0):
     rows, e_start, e_lens = torch.empty(T * k, **i64), torch.empty(E, **i64), torch.empty(E, **i64)
     sg.sgmv_route(logits, weights, chosen, slots, rows, e_start, e_lens, renormalize=True)
     # the experts on their rows; nothing of the routing comes back to the host
-    hidden = torch.empty(T * k, w.down.shape[2], dtype=x.dtype, device=dev)
-    sg.sgmv_grouped_gemm(x, w.gate_up, hidden, e_start, e_lens, None, E, T, row_indices_tensor=rows, gated=True)
+    gate_up = w.gate_up[0] if isinstance(w.gate_up, tuple) else w.gate_up
+    hidden = torch.empty(T * k, gate_up.shape[1] // 2, dtype=x.dtype, device=dev)
+    experts(x, w.gate_up, hidden, e_start, e_lens, None, E, T, row_indices_tensor=rows, gated=True)
     out = torch.empty(T * k, H, dtype=x.dtype, device=dev)
-    sg.sgmv_grouped_gemm(hidden, w.down, out, e_start, e_lens, None, E, T)
+    experts(hidden, w.down, out, e_start, e_lens, None, E, T)
     sg.sgmv_combine(out, weights, slots, residual, add_inputs=True)
+    if seen is not None:
+        seen.update(projected=projected, x=x, weights=weights, chosen=chosen, slots=slots, rows=rows, start=e_start, lens=e_lens,
+                    hidden=hidden, out=out)
     return chosen
 
 
@@ -95,8 +135,8 @@ def block_in_64_bits(w, attn, residual, start, lens, adapter, chosen, scale=2.0)
 
 
 def main():
-    hidden, width, experts, adapters, rank, top_k = 1024, 512, 16, 6, 16, 4
-    w = random_weights(hidden, width, experts, adapters, rank)
+    hidden, width, count, adapters, rank, top_k = 1024, 512, 16, 6, 16, 4
+    w = random_weights(hidden, width, count, adapters, rank)
     g = torch.Generator(device="cuda").manual_seed(1)
     for name, lens in (("decode, 24 requests", [1] * 24), ("prefill, 5 prompts", [130, 1, 77, 300, 64])):
         T = sum(lens)
@@ -109,7 +149,16 @@ def main():
         chosen = block(w, attn, residual, start, lens_t, adapter, top_k)
         want = block_in_64_bits(w, attn, before, start, lens_t, adapter, chosen)
         off = float((residual.double() - want).norm() / want.norm())
-        print(f"{name}: {T} tokens, {top_k} of {experts} experts each, relative difference from 64 bits {off:.2e}")
+        print(f"{name}: {T} tokens, {top_k} of {count} experts each, relative difference from 64 bits {off:.2e}")
+        # The 4-bit weights beside the 16-bit ones they were made of, in the same 64-bit form: what is left is
+        # the rounding of the activations to 4 bits.
+        q = four_bit(w)
+        residual = before.clone()
+        chosen = block(q, attn, residual, start, lens_t, adapter, top_k)
+        read = replace(w, proj=unpacked(q.proj, w.proj), gate_up=unpacked(q.gate_up, w.gate_up), down=unpacked(q.down, w.down))
+        want = block_in_64_bits(read, attn, before, start, lens_t, adapter, chosen)
+        off = float((residual.double() - want).norm() / want.norm())
+        print(f"    with 4-bit weights and activations, from its weights in 64 bits {off:.2e}")
 
 
 if __name__ == "__main__":
