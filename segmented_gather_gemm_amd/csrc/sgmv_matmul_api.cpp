@@ -412,6 +412,16 @@ bool projects_by_token(const sgmv::MatmulParams& p, const sgmv_shrink_slice* dow
   return true;
 }
 
+// Whether the few-row kernel's workgroups each do all of these projections, which saves a launch.
+// Measured, us a call, that and a launch of their own, hidden 4096: rank 16, 4096
+// columns, one token 11.7 and 13.6, two 11.5 and 13.5, four 16.5 and 13.6; QKV,
+// one token 14.9 and 17.3, two 18.2 and 17.3; rank 64 16.6 and 13.7; hidden
+// 14336, rank 16 22.7 and 25.9.
+bool projects_itself(const sgmv::MatmulParams& p, const Plan& plan, const sgmv_matrix& x) {
+  const int64_t rows = p.T * p.num_slices * p.K;
+  return plan.quantises && rows <= sgmv::kMxProjectMost && rows * x.cols <= 1 << 18;
+}
+
 // Those projections and, unless the kernel does that itself, the inputs' codes and scales.
 sgmv_status project_by_token(sgmv::MatmulParams& p, const Plan& plan, const sgmv_shrink_slice* down,
                              const sgmv_matrix& x, const Quantised& q, void* workspace, float scale,
@@ -674,6 +684,13 @@ sgmv_status sgmv_mx_lora_linear(sgmv_matrix inputs, sgmv_mx_stack weight, const 
   st = make_plan(p, x.dtype, false, &plan, &x);
   if (st != SGMV_OK) return st;
   if (p.num_slices > 0 && projects_by_token(p, down, x)) {
+    if (projects_itself(p, plan, x)) {
+      quantise_inputs(p, plan, x, q, workspace, stream);
+      p.projects = 1;
+      p.scale = scale;
+      for (int i = 0; i < p.num_slices; ++i) p.s[i].v = static_cast<const float*>(down[i].lora_a.data);
+      return launch(plan, p, stream);
+    }
     st = project_by_token(p, plan, down, x, q, workspace, scale, stream);
     if (st != SGMV_OK) return st;
     return launch(plan, p, stream);

@@ -59,6 +59,8 @@ struct MatmulParams {
   int64_t xs_row_bytes;
   int64_t ws_row_bytes;
   int32_t mx_hidden;      // mx: values of an input row, where x has them in 16 bits
+  int32_t projects;       // mx_skinny: AdapterDesc::v holds lora_A, the kernel projects onto it
+  float scale;            // of those projections
 };
 
 // Generic kernel: any size, stride and alignment (64 x 64 tiles).
@@ -86,6 +88,8 @@ TiledKernel matmul_skinny_64_adapted(int wd);
 // eight), and 32 or 64 of a dense call, quantised before.  A workgroup walks over tiles of 16 columns, col_tiles of
 // the launch apart.
 constexpr int kMxSkinnyWaves = 8;
+// Rows of lora_A, over a call's tokens, that each workgroup projects onto itself.
+constexpr int kMxProjectMost = 48;
 TiledKernel mx_skinny(int wd, int mode, int rows, int64_t groups);
 
 }  // namespace sgmv

@@ -117,5 +117,12 @@ __device__ __forceinline__ void mx_values8(uint32_t codes, uint32_t scale, u32x4
   }
 }
 
+// The sum of a value over the wave, in all lanes.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
 }  // namespace dev
 }  // namespace sgmv

@@ -118,13 +118,6 @@ __global__ __launch_bounds__(kMxThreads) void mx_dequantize(MxParams p) {
   }
 }
 
-// The sum of a value over the wave, in all lanes.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
 // One token and 16 rows of its adapter's lora_A for a slice: a wave has two of
 // the rows and the token's values, eight a lane and 512 at a time, so that all
 // of a row's loads are in flight together.  Bound by their latency: for a
@@ -133,7 +126,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // matrix unit, take 3.7 and 11 us.
 template <int XD>
 __global__ __launch_bounds__(64 * kMxProjectWaves) void mx_project(MxProjectParams p) {
-  constexpr int kAhead = 8;  // blocks of a lane at a time
+  constexpr int kAhead = kMxProjectAhead;
   __shared__ int32_t adapter;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int part = blockIdx.x % p.parts, slice = blockIdx.x / p.parts, t = blockIdx.y;

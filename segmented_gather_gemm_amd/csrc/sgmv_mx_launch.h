@@ -60,6 +60,8 @@ struct MxProjectParams {
   float* v[SGMV_MAX_SLICES];       // (T, v_stride)
 };
 constexpr int kMxProjectWaves = 8, kMxProjectRows = 2 * kMxProjectWaves;
+constexpr int kMxProjectAhead = 8;                        // blocks of eight values of a lane at a time
+constexpr int kMxProjectStep = kMxProjectAhead * 64 * 8;  // values
 const void* mx_project_kernel(int xd);
 
 // Quantise the rows of `x` into codes and scales (shapes checked by the caller).

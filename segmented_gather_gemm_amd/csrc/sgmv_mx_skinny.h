@@ -4,22 +4,31 @@
 //
 // A few rows against a whole weight matrix are bound by reading the weights
 // once.  A workgroup of eight waves keeps its 16 MB input rows in registers
-// and walks over tiles of 16 weight rows (output columns); the
-// contraction is dealt to the waves in chunks of two groups (256 values, 128
-// bytes of codes a row), chunk c to wave c mod 8.  Up to 16 rows are quantised
-// here: a lane's share of a matrix
-// instruction's input rows is one whole block of 32 values of one row, so that
-// this needs no exchange between lanes.  Loads of the next tile are in
-// flight while a tile's eight partial sums meet in LDS and are added in order
+// and walks over tiles of 16 weight rows (output columns); the contraction is
+// dealt to the waves in chunks of two groups (256 values, 128 bytes of codes a
+// row), chunk c to wave c mod 8.  Up to 16 rows are quantised here: a lane's share
+// of a matrix instruction's input rows is one whole block of 32 values of one
+// row, so that this needs no exchange between lanes.  Loads of the next tile are
+// in flight while a tile's eight partial sums meet in LDS and are added in order
 // (two sets of them, one barrier a tile).
 //
 // Adapters: each result's part is summed in float32 on the vector unit, a row
 // with its own adapter, in order of k: for the few rows of a decode batch that is
-// less than gathering the rows of each adapter for the matrix unit.
+// less than gathering the rows of each adapter for the matrix unit.  One or two
+// tokens' projections are made here as well.
+//
+// Measured, hidden 4096, bfloat16: 4096 columns, one token 6.8 us, with its
+// adapter of rank 16 10.2 (of which 3.4 its projection, a chain of two loads from
+// memory and a sum over the wave; a launch of its own takes 4.5 and the gap);
+// 28672 columns (62 MB of codes and scales), 1 and 16 rows 15.4 and 17.7 us, 4.0
+// and 3.5 TB/s; 64 rows of 32 adapters, QKV's 6144 columns, 13.2 us, of which reading
+// the weights would take 2.6: bound by the latency of a tile's reads, of which a
+// workgroup has one or two tiles here.
 #pragma once
 
 #include "sgmv_matmul.h"
 #include "sgmv_mx.h"
+#include "sgmv_mx_launch.h"
 
 namespace sgmv {
 namespace dev {
@@ -42,16 +51,16 @@ __device__ __forceinline__ void row_adapters(const MatmulParams& p, Segment seg,
   __syncthreads();
 }
 
-// sum_k v[row][k] b[a][n][k] over the slice that holds column n, in order of k (0
-// without an adapter or such a slice).  Whole blocks of eight, aligned.
-template <int WD>
-__device__ __forceinline__ float adapter_product(const MatmulParams& p, int32_t row, int32_t a, int n) {
+// sum_k v(row, s)[k] b[a][n][k] over the slice s that holds column n, in order of k
+// (0 without an adapter or such a slice).  Whole blocks of eight, aligned.
+template <int WD, class V>
+__device__ __forceinline__ float adapter_product(const MatmulParams& p, int32_t a, int n, V v_of) {
   float sum = 0.f;
   for (int s = 0; s < p.num_slices; ++s) {
     const AdapterDesc d = adapter_desc(s);
     if (a < 0 || n < d.offset || n >= d.offset + d.n) continue;
     const int64_t at = ((int64_t)a * d.n + n - d.offset) * p.K;
-    const float* vr = d.v + (int64_t)row * p.v_stride;
+    const float* vr = v_of(d, s);
 #pragma unroll 2
     for (int k = 0; k < p.K; k += 8) {
       u32x4 bv, raw[2];
@@ -67,6 +76,58 @@ __device__ __forceinline__ float adapter_product(const MatmulParams& p, int32_t 
   return sum;
 }
 
+// projected[row][slice][k] = scale * x[row] . lora_A[adapter][k] for the slices that
+// this workgroup's columns are in: a wave two k at a time (four: one token's
+// QKV 16.4 against 14.9 us), lora_A (in v's place) and x in blocks of eight a
+// lane; the order of a sum is mx_project's.  Every workgroup does that for itself.
+template <int WD>
+__device__ __forceinline__ void project_rows(const MatmulParams& p, const TileLoc& loc, int tiles,
+                                             const int32_t* adapter, float* projected) {
+  constexpr int R = 2;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int count = (loc.end - loc.row) * p.num_slices * p.K;
+  for (int i = R * wave; i < count; i += R * kMxSkinnyWaves) {
+    const int rs = i / p.K, k = i - rs * p.K, r = rs / p.num_slices;
+    const AdapterDesc d = adapter_desc(rs - r * p.num_slices);
+    const int a = uniform(adapter[r]);
+    bool used = false;
+    for (int tile = loc.col; tile < tiles; tile += p.col_tiles)
+      used = used || (tile * 16 < d.offset + d.n && tile * 16 + 16 > d.offset);
+    if (a < 0 || !used) continue;
+    const char* x = static_cast<const char*>(p.x) + (loc.row + r) * p.x_row_bytes;
+    const char* la = reinterpret_cast<const char*>(d.v) + ((int64_t)a * p.K + k) * p.mx_hidden * 2;
+    float sum[R] = {};
+    for (int base = 0; base < p.mx_hidden; base += kMxProjectStep) {
+      u32x4 xv[kMxProjectAhead], av[R][kMxProjectAhead];
+#pragma unroll
+      for (int j = 0; j < kMxProjectAhead; ++j) {
+        const int64_t at = base + (j * 64 + lane) * 8;
+        const bool in = at < p.mx_hidden;
+        xv[j] = in ? *reinterpret_cast<const u32x4*>(x + at * 2) : u32x4{};
+#pragma unroll
+        for (int h = 0; h < R; ++h)
+          av[h][j] = in ? *reinterpret_cast<const u32x4*>(la + (h * (int64_t)p.mx_hidden + at) * 2) : u32x4{};
+      }
+#pragma unroll
+      for (int j = 0; j < kMxProjectAhead; ++j) {
+        float xf[8], f[8];
+        out_values<WD>(&xv[j], xf);
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          out_values<WD>(&av[h][j], f);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) sum[h] = fmaf(xf[q], f[q], sum[h]);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      const float v = wave_sum(sum[h]) * p.scale;
+      if (lane == 0) projected[i + h] = v;
+    }
+  }
+}
+
 // C: chunks of a wave that it holds at a time; longer contractions take several
 // such sets (and read their inputs again for each tile).
 template <int WD, int MODE, int MB, int C>
@@ -78,6 +139,8 @@ __global__ __launch_bounds__(64 * kMxSkinnyWaves, 2) void mx_skinny_rows(MatmulP
   __shared__ int32_t sh[kW + 4];
   __shared__ float part[2][kW][kBlocks][16][kPad];
   __shared__ int32_t row_adapter[MODE == kAdapted ? ROWS : 1];
+  constexpr bool kProjects = kQuantise && MODE == kAdapted;
+  __shared__ __attribute__((aligned(16))) float projected[kProjects ? kMxProjectMost : 1];
   const TileLoc loc = find_tile<kNT>(p, ROWS, sh);
   if (loc.row < 0) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -180,6 +243,12 @@ __global__ __launch_bounds__(64 * kMxSkinnyWaves, 2) void mx_skinny_rows(MatmulP
   read_w(loc.col, 0);
   if constexpr (MODE == kAdapted)
     row_adapters<kNT, ROWS>(p, seg, loc.row, loc.end, row_adapter);
+  if constexpr (kProjects) {
+    if (p.projects) {
+      project_rows<WD>(p, loc, tiles, row_adapter, projected);
+      __syncthreads();
+    }
+  }
 
   constexpr int kMine = (ROWS * 16 + kNT - 1) / kNT;  // results of a thread in a tile
   int buffer = 0;
@@ -212,7 +281,17 @@ __global__ __launch_bounds__(64 * kMxSkinnyWaves, 2) void mx_skinny_rows(MatmulP
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int e = threadIdx.x + i * kNT, r = e / 16;
-        extra[i] = r < rows ? adapter_product<WD>(p, loc.row + r, row_adapter[r], tile * 16 + e % 16) : 0.f;
+        extra[i] = 0.f;
+        if (r >= rows) continue;
+        const int a = row_adapter[r], n = tile * 16 + e % 16;
+        if (kProjects && p.projects)
+          extra[i] = adapter_product<WD>(p, a, n, [&](const AdapterDesc&, int s) {
+            return &projected[(r * p.num_slices + s) * p.K];
+          });
+        else
+          extra[i] = adapter_product<WD>(p, a, n, [&](const AdapterDesc& d, int) {
+            return d.v + (int64_t)(loc.row + r) * p.v_stride;
+          });
       }
     }
     __syncthreads();

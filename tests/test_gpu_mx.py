@@ -205,6 +205,15 @@ def test_lora_linear_ranks(T, K):
     lora_case(T, 320, [192], K, 3, [T // 2, T // 2], [0, 2], seed=K)
 
 
+@pytest.mark.parametrize("T,K,widths,idx", [(1, 16, [200], [2]), (1, 16, [40, 8, 600], [0]), (1, 8, [16, 16], [-1]), (2, 24, [72], [1, 1]),
+                                            (2, 8, [1040, 520, 24], [2, 0]), (3, 16, [136], [1, -1, 0]), (6, 8, [5000], [0, 1, 2, 0, 1, 2])])
+@pytest.mark.parametrize("H", [8, 520, 4096, 4104, 5000])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F16, F32)])
+def test_lora_linear_projects_in_the_product(T, K, widths, idx, H, dtype, out):
+    """At most 48 rows of lora_A over the tokens: each workgroup of the product projects onto them itself."""
+    lora_case(T, H, widths, K, 3, [1] * T, idx, dtype=dtype, out=out, bias=H == 520, add=T == 2, seed=H + T, pad_x=8, gaps=[8])
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("out", [BF16, F16, F32])
 @pytest.mark.parametrize("T,add", [(7, False), (7, True), (50, True), (190, False), (190, True), (400, True)])
