@@ -5,9 +5,9 @@
 // exchanges inside a quad of lanes, loads and stores are consecutive over the
 // lanes, and a group's four scale bytes leave as one word.  Groups are dealt to
 // the lanes over all rows, whatever a row's length.  Bound by memory: 16384 x
-// 4096 bfloat16 values 31.0 us = 5.5 TB/s, 28672 x 4096 float32 ones 96 us = 5.5
-// TB/s (a copy of 1 GiB 5.1); kMxUnroll groups a lane, two against one, four
-// and eight: 31.0, 32.6, 31.9 and 33.0 us.
+// 4096 bfloat16 values 31.0 us = 5.5 TB/s, 28672 x 4096 float32 ones 110 us = 4.8
+// TB/s and back to bfloat16 55 us = 5.4 TB/s (a copy of 1 GiB 5.1); kMxUnroll
+// groups a lane, two against one, four and eight: 31.0, 32.6, 31.9 and 33.0 us.
 #include "sgmv_mx.h"
 #include "sgmv_mx_launch.h"
 
