@@ -118,12 +118,12 @@ __global__ __launch_bounds__(kMxThreads) void mx_dequantize(MxParams p) {
   }
 }
 
-// One token and 16 rows of its adapter's lora_A for a slice: a wave has two of
+// One token and eight rows of its adapter's lora_A for a slice: a wave has one of
 // the rows and the token's values, eight a lane and 512 at a time, so that all
-// of a row's loads are in flight together.  Bound by their latency: for a
-// decode batch of 64 tokens, 32 adapters and three slices of rank 16 (hidden
-// 4096) the kernels it replaces, which gather each adapter's tokens for the
-// matrix unit, take 3.7 and 11 us.
+// of a row's loads are in flight together.  Bound by their latency: a decode
+// batch of 64 tokens, 32 adapters and three slices of rank 16 (hidden 4096) takes
+// 7.6 us (two rows a wave 8.4); the kernels it replaces, which gather each
+// adapter's tokens for the matrix unit, 3.7 and 11.
 template <int XD>
 __global__ __launch_bounds__(64 * kMxProjectWaves) void mx_project(MxProjectParams p) {
   constexpr int kAhead = kMxProjectAhead;
@@ -153,24 +153,22 @@ __global__ __launch_bounds__(64 * kMxProjectWaves) void mx_project(MxProjectPara
   __syncthreads();
   const int a = uniform(adapter);
   if (a < 0 && !quantise) return;
-  const int k0 = part * kMxProjectRows + wave * 2;
-  const bool have0 = a >= 0 && k0 < p.K, have1 = a >= 0 && k0 + 1 < p.K;
+  const int k0 = part * kMxProjectRows + wave;
+  const bool have = a >= 0 && k0 < p.K;
   // p.a and p.v by a variable index would be copied to scratch memory.
   typedef const __attribute__((address_space(4))) MxProjectParams* Args;
   const Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
   const int64_t row_bytes = (int64_t)p.H * 2;
   const char* la = static_cast<const char*>(args->a[slice]) + ((int64_t)(a < 0 ? 0 : a) * p.K + k0) * row_bytes;
-  float s0 = 0.f, s1 = 0.f;
+  float sum = 0.f;
   for (int base = 0; base < groups * 16; base += 64 * kAhead) {
-    u32x4 a0[kAhead], a1[kAhead];
+    u32x4 av[kAhead];
     if (base > 0) read_x(base);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int at = (base + i * 64 + lane) * 8;
-      const bool in = at < p.H;
-      a0[i] = a1[i] = u32x4{};
-      if (in && have0) a0[i] = *reinterpret_cast<const u32x4*>(la + (int64_t)at * 2);
-      if (in && have1) a1[i] = *reinterpret_cast<const u32x4*>(la + row_bytes + (int64_t)at * 2);
+      av[i] = u32x4{};
+      if (at < p.H && have) av[i] = *reinterpret_cast<const u32x4*>(la + (int64_t)at * 2);
     }
     // A wave quantises one block a lane, whole groups of the row.
 #pragma unroll
@@ -191,21 +189,13 @@ __global__ __launch_bounds__(64 * kMxProjectWaves) void mx_project(MxProjectPara
     for (int i = 0; i < kAhead; ++i) {
       float xf[8], f[8];
       out_values<XD>(xv[i], xf);
-      out_values<XD>(&a0[i], f);
+      out_values<XD>(&av[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s0 = fmaf(xf[j], f[j], s0);
-      out_values<XD>(&a1[i], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s1 = fmaf(xf[j], f[j], s1);
+      for (int j = 0; j < 8; ++j) sum = fmaf(xf[j], f[j], sum);
     }
   }
-  s0 = wave_sum(s0) * p.scale;
-  s1 = wave_sum(s1) * p.scale;
-  if (lane == 0) {
-    float* v = args->v[slice] + (int64_t)t * p.v_stride + k0;
-    if (have0) v[0] = s0;
-    if (have1) v[1] = s1;
-  }
+  sum = wave_sum(sum) * p.scale;
+  if (lane == 0 && have) args->v[slice][(int64_t)t * p.v_stride + k0] = sum;
 }
 
 }  // namespace dev

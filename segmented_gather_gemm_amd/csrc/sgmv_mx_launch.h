@@ -59,7 +59,7 @@ struct MxProjectParams {
   const void* a[SGMV_MAX_SLICES];  // lora_A (L, K, H) contiguous, 16-byte aligned
   float* v[SGMV_MAX_SLICES];       // (T, v_stride)
 };
-constexpr int kMxProjectWaves = 8, kMxProjectRows = 2 * kMxProjectWaves;
+constexpr int kMxProjectWaves = 8, kMxProjectRows = kMxProjectWaves;
 constexpr int kMxProjectAhead = 8;                        // blocks of eight values of a lane at a time
 constexpr int kMxProjectStep = kMxProjectAhead * 64 * 8;  // values
 const void* mx_project_kernel(int xd);
