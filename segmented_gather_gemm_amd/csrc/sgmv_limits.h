@@ -175,5 +175,9 @@ constexpr uint32_t divide(uint32_t n, const Divisor& d) {
 constexpr int64_t mx_groups(int64_t values) { return (values + 127) / 128; }
 constexpr int64_t kMxCodeBytes = 64, kMxScaleBytes = 4;
 
+// Row r of matrix e of a stack of matrices of `rows` rows.  In 64 bits from the
+// first product on: 2^30 matrices and more of two rows fit a device's memory.
+constexpr int64_t stack_row(int64_t e, int64_t rows, int64_t r) { return e * rows + r; }
+
 }  // namespace limits
 }  // namespace sgmv

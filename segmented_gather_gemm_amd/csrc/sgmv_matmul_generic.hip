@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kThreads) void matmul_generic(MatmulParams p) {
             wv = *reinterpret_cast<const u32x4*>(wm + r * p.w_row_bytes + g * 64 + q * 16);
             sw = *reinterpret_cast<const uint32_t*>(
                      static_cast<const char*>(p.ws) +
-                     (loc.e * (GATED ? 2 : 1) * (int64_t)p.N + r) * p.ws_row_bytes + g * 4) >> (8 * q);
+                     limits::stack_row(loc.e, (GATED ? 2 : 1) * (int64_t)p.N, r) * p.ws_row_bytes + g * 4) >> (8 * q);
           }
           acc[t][f] = mfma_fp4<0>(wv, xv, acc[t][f], sw, sx);
         }

@@ -273,7 +273,7 @@ __global__ __launch_bounds__(S::kNT, S::kOccupancy) void matmul_tiled(MatmulPara
         const int64_t nr = left < HN ? left : HN;
         constexpr int kMats = MODE == kGated ? 2 : 1;
         sr[j] = uniform_rsrc(static_cast<const char*>(p.ws) +
-                                 (loc.e * (int64_t)kMats * p.N + first) * p.ws_row_bytes,
+                                 limits::stack_row(loc.e, kMats * (int64_t)p.N, first) * p.ws_row_bytes,
                              nr <= 0 ? 0 : (nr - 1) * p.ws_row_bytes + p.H / 8);
         soff[j] = (uint32_t)((int64_t)n * p.ws_row_bytes);
       }

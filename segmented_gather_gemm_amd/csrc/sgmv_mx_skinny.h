@@ -219,7 +219,7 @@ __global__ __launch_bounds__(64 * kMxSkinnyWaves, 2) void mx_skinny_rows(MatmulP
     const int64_t nr = p.N - n0 < 16 ? p.N - n0 : 16;  // none past the last tile
 #pragma unroll
     for (int t = 0; t < kMats; ++t) {
-      const int64_t first = (loc.e * (int64_t)kMats + t) * p.N + n0;
+      const int64_t first = limits::stack_row(loc.e, kMats * (int64_t)p.N, t * (int64_t)p.N + n0);
       const rsrc_t wr = uniform_rsrc(static_cast<const char*>(p.w) + first * p.w_row_bytes,
                                      nr <= 0 ? 0 : (nr - 1) * p.w_row_bytes + (int64_t)p.H * 2);
       const rsrc_t sr = uniform_rsrc(static_cast<const char*>(p.ws) + first * p.ws_row_bytes,

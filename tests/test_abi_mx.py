@@ -241,3 +241,22 @@ def test_the_definition_itself():
     codes, scales = M.quantize(nan)
     assert scales[0, 0] == 255 and not codes.any() and bool(M.values(codes, scales, 32).isnan().all())
     assert ctypes.sizeof(MxStack) == 56 and np.array_equal(M.GRID[:3], [0, .5, 1])
+
+
+STACK = r"""
+#include <stdio.h>
+#include "sgmv_limits.h"
+int main() {
+  const int32_t e = 1 << 30, n = 1 << 29;  // as the kernels hold them
+  printf("%lld %lld\n", (long long)sgmv::limits::stack_row(e, 2 * (int64_t)1, 1), (long long)sgmv::limits::stack_row(7, 2 * (int64_t)n, n));
+}
+"""
+
+
+def test_rows_of_a_stack_past_32_bits(tmp_path):
+    """A stack of 2^30 experts of two rows (the gate's and the other factor's) is 137 GB of codes: its last rows' numbers."""
+    src, exe = tmp_path / "stack.cpp", str(tmp_path / "stack")
+    src.write_text(STACK)
+    subprocess.run(["g++", "-std=c++17", "-O1", f"-I{CSRC}", str(src), "-o", exe], check=True)
+    out = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()
+    assert [int(v) for v in out] == [2 ** 31 + 1, 7 * 2 ** 30 + 2 ** 29]
