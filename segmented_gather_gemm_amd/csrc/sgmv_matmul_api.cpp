@@ -132,7 +132,14 @@ sgmv::TiledKernel pick_mx_tiled(const sgmv::MatmulParams& p, int wd, int mode, i
 // rank 64, 28672 columns 73 and 90, 131 and 112, 232 and 119.  Experts: 16 used
 // by a row each, hidden 2048, 2 x 1408 columns 14.5 and 14.9, 64 of 4 rows 46.9 and
 // 50.9, of 16 rows 66 and 54; hidden 14336, 4096 columns, 8 of one row 124 and 54
-// (the inputs are quantised again for every tile).
+// (the inputs are quantised again for every tile).  Up to 16 rows take it whatever
+// their adapters.  Both with all of a call's launches, ranks 16, 64, 128 and 256, 4096
+// columns: one row 10.5 and 20.0, 11.9 and 21.1, 12.4 and 23.4, 14.3 and 28.1, 16 rows of as
+// many adapters 13.7 and 28.9, 17.1 and 54.7, 20.6 and 86.9, 27.4 and 150.5; 28672 columns:
+// one row 25.6 and 25.4, 30.0 and 26.2, 36.8 and 28.8, 51.4 and 34.2, 16 rows of one adapter
+// 29.5 and 28.8, 38.8 and 28.6, 50.2 and 31.4, 72.6 and 38.9, of 16 adapters 31.3 and 35.7,
+// 42.9 and 56.6, 59.0 and 89.5, 93.5 and 154.6: it loses where a wide projection's rows
+// share few adapters of rank 64 and more.
 sgmv::TiledKernel mx_few(const sgmv::MatmulParams& p, const sgmv_matrix& x, int mode, int cus,
                          bool* quantises) {
   using namespace sgmv;

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kMxThreads) void mx_dequantize(MxParams p) {
 // the rows and the token's values, eight a lane and 512 at a time, so that all
 // of a row's loads are in flight together.  Bound by their latency: a decode
 // batch of 64 tokens, 32 adapters and three slices of rank 16 (hidden 4096) takes
-// 7.6 us (two rows a wave 8.4); the kernels it replaces, which gather each
+// 7.2-7.6 us (two rows a wave 8.4); the kernels it replaces, which gather each
 // adapter's tokens for the matrix unit, 3.7 and 11.
 template <int XD>
 __global__ __launch_bounds__(64 * kMxProjectWaves) void mx_project(MxProjectParams p) {

@@ -18,12 +18,13 @@
 // tokens' projections are made here as well.
 //
 // Measured, hidden 4096, bfloat16: 4096 columns, one token 6.8 us, with its
-// adapter of rank 16 10.2 (of which 3.4 its projection, a chain of two loads from
+// adapter of rank 16 10.2-10.5 (of which 3.4 its projection, a chain of two loads from
 // memory and a sum over the wave; a launch of its own takes 4.5 and the gap);
 // 28672 columns (62 MB of codes and scales), 1 and 16 rows 15.4 and 17.7 us, 4.0
-// and 3.5 TB/s; 64 rows of 32 adapters, QKV's 6144 columns, 13.2 us, of which reading
-// the weights would take 2.6: bound by the latency of a tile's reads, of which a
-// workgroup has one or two tiles here.
+// and 3.5 TB/s; 64 rows of 32 adapters, QKV's 6144 columns, 13.2-13.7 us, of which reading
+// the weights would take 2.6: bound by latency.  A workgroup has three tiles here, the
+// weights of one ahead, and as loads arrive in order, a tile's lora_B arrives
+// behind the next tile's weights.
 #pragma once
 
 #include "sgmv_matmul.h"
